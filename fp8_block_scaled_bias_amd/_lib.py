@@ -68,6 +68,19 @@ SIGNATURES = {
     "grouped_fp8_gemm_swiglu_keep": (ctypes.c_int, [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _i32, _i64,
                                                     _i64, _i64, _vp, _vp, _vp, _vp]),
     "moe_combine": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i32, _i64, _vp, _vp]),
+    "moe_router_logits": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i32, _vp, _vp, _sz, _vp]),
+    "moe_router_logits_backward": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i32, _vp, _vp, _vp,
+                                                  _vp, _sz, _vp]),
+    "moe_gate": (ctypes.c_int, [_vp, _i32, _i64, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32,
+                                _vp, _vp, _vp, _vp, _vp]),
+    "moe_gate_backward": (ctypes.c_int, [_vp, _i32, _i64, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp,
+                                         _vp, _vp]),
+    "int8_quant_rows": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "int8_quant_channels": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "grouped_int8_gemm": (ctypes.c_int, [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _i32, _i64, _i64, _i64,
+                                         _vp, _vp]),
+    "grouped_int8_gemm_swiglu": (ctypes.c_int, [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _i32, _i64, _i64,
+                                                _i64, _vp, _vp]),
 }
 
 MOE_OK = 0
@@ -75,6 +88,10 @@ MOE_ERR_INVALID = -1
 MOE_ERR_UNSUPPORTED = -2
 MOE_ERR_HIP = -3
 MOE_ERR_WORKSPACE = -4
+
+# element types and score functions of the gate
+TYPE_F32, TYPE_BF16 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
 _lib = None
 
@@ -310,3 +327,60 @@ def moe_combine(expert_out_bf16, inv_perm, topk_w, shared_out_bf16, T, k, H, y_b
                 stream=None):
     return _call("moe_combine", _dev(expert_out_bf16), _dev(inv_perm), _dev(topk_w),
                  _dev(shared_out_bf16), T, k, H, _dev(y_bf16), _stream(stream))
+
+
+def _logits_type(t):
+    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("logits must be a float32 or bfloat16 torch.Tensor")
+    return TYPE_F32 if t.dtype == torch.float32 else TYPE_BF16
+
+
+def moe_router_logits(x_bf16, T, H, centroids, E, logits, workspace, workspace_bytes, stream=None):
+    return _call("moe_router_logits", _dev(x_bf16), T, H, _dev(centroids), E, _dev(logits),
+                 _dev(workspace), workspace_bytes, _stream(stream))
+
+
+def moe_router_logits_backward(x_bf16, centroids, d_logits, T, H, E, dx_in_bf16, dx_out_bf16,
+                               d_centroids, workspace, workspace_bytes, stream=None):
+    return _call("moe_router_logits_backward", _dev(x_bf16), _dev(centroids), _dev(d_logits), T, H, E,
+                 _dev(dx_in_bf16), _dev(dx_out_bf16), _dev(d_centroids), _dev(workspace),
+                 workspace_bytes, _stream(stream))
+
+
+def moe_gate(logits, T, E, bias, score, n_group, topk_group, group_top, k, renormalize, scale,
+             topk_idx, topk_w, expert_counts, stream=None, *, scores=None):
+    return _call("moe_gate", _dev(logits), _logits_type(logits), T, E, _dev(bias), score, n_group,
+                 topk_group, group_top, k, int(renormalize), scale, _dev(topk_idx), _dev(topk_w),
+                 _dev(expert_counts), _dev(scores), _stream(stream))
+
+
+def moe_gate_backward(logits, T, E, score, k, renormalize, scale, topk_idx, d_topk_w, d_logits,
+                      stream=None, *, d_scores=None):
+    if isinstance(d_logits, torch.Tensor) and d_logits.dtype != logits.dtype:
+        raise TypeError("d_logits must have the logits' type")
+    return _call("moe_gate_backward", _dev(logits), _logits_type(logits), T, E, score, k,
+                 int(renormalize), scale, _dev(topk_idx), _dev(d_topk_w), _dev(d_scores),
+                 _dev(d_logits), _stream(stream))
+
+
+def int8_quant_rows(in_bf16, M, K, ld_in, out_int8, scales, stream=None):
+    return _call("int8_quant_rows", _dev(in_bf16), M, K, ld_in, _dev(out_int8), _dev(scales),
+                 _stream(stream))
+
+
+def int8_quant_channels(w_f32, G, N, K, out_int8, scales, stream=None):
+    return _call("int8_quant_channels", _dev(w_f32), G, N, K, _dev(out_int8), _dev(scales),
+                 _stream(stream))
+
+
+def grouped_int8_gemm(A, A_scale, a_row_index, B, B_scale, group_offsets, G, M_total, N, K, C_bf16,
+                      stream=None):
+    return _call("grouped_int8_gemm", _dev(A), _dev(A_scale), _dev(a_row_index), _rows(A), _dev(B),
+                 _dev(B_scale), _dev(group_offsets), G, M_total, N, K, _dev(C_bf16), _stream(stream))
+
+
+def grouped_int8_gemm_swiglu(A, A_scale, a_row_index, B, B_scale, group_offsets, G, M_total, I, K,
+                             H_bf16, stream=None):
+    return _call("grouped_int8_gemm_swiglu", _dev(A), _dev(A_scale), _dev(a_row_index), _rows(A),
+                 _dev(B), _dev(B_scale), _dev(group_offsets), G, M_total, I, K, _dev(H_bf16),
+                 _stream(stream))

@@ -27,6 +27,7 @@
 //     expert and workgroup (integer adds: order-independent, so
 //     deterministic).
 //  3. bias_update: the +-gamma rule on the counts.
+//  4. sum_partials: the logits themselves, for the gate of gate.hip.
 #include "common.h"
 
 namespace moe {
@@ -563,6 +564,16 @@ __global__ __launch_bounds__(256) void router_select_kernel(
   }
 }
 
+// logits[i] = sum of the split-K partials of element i, in their order
+__global__ __launch_bounds__(256) void sum_partials_kernel(const float* __restrict__ part, int KS,
+                                                           int64_t n, float* __restrict__ logits) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    float s = part[i];
+    for (int u = 1; u < KS; ++u) s += part[u * n + i];
+    logits[i] = s;
+  }
+}
+
 __global__ __launch_bounds__(256) void bias_update_kernel(const int32_t* __restrict__ counts,
                                                           float* __restrict__ bias, int E,
                                                           float gamma) {
@@ -628,6 +639,24 @@ extern "C" size_t moe_route_workspace_bytes(int64_t T, int64_t H, int32_t E) {
 
 namespace {
 
+// the split-K partials of the logits [ks, T, E] into part (the workspace's
+// start, or any other place when there is one split)
+void launch_logits(const RouteSplit& sp, const void* x_bf16, int64_t T, int64_t H,
+                   const float* centroids, int32_t E, void* workspace, float* part, hipStream_t st) {
+  const uint16_t* x = static_cast<const uint16_t*>(x_bf16);
+  if (sp.wide) {
+    uint16_t* planes = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) +
+                                                   route_ws_partials(sp, T, E));
+    split_planes_kernel<<<dim3(1024), dim3(256), 0, st>>>(centroids, (int64_t)E * H, planes);
+    router_logits_wide_kernel<<<dim3((unsigned)ceil_div(T, RW_TOK), (unsigned)sp.ks), dim3(512), 0,
+                                st>>>(x, T, H, planes, E, sp.kper, part);
+  } else {
+    router_logits_kernel<<<dim3((unsigned)ceil_div(T, RT_TOK), (unsigned)ceil_div(E, RT_EXP),
+                                (unsigned)sp.ks),
+                           dim3(256), 0, st>>>(x, T, H, centroids, E, sp.kper, part);
+  }
+}
+
 int route_impl(const void* x_bf16, int64_t T, int64_t H, const float* centroids,
                const float* bias, int32_t E, int32_t n_group, int32_t topk_group, int32_t k,
                int32_t* topk_idx, float* topk_w, int32_t* expert_counts, void* workspace,
@@ -669,19 +698,7 @@ int route_impl(const void* x_bf16, int64_t T, int64_t H, const float* centroids,
   float* part = static_cast<float*>(workspace);
 
   fill_i32_kernel<<<1, 256, 0, st>>>(expert_counts, E, 0);
-  if (sp.wide) {
-    uint16_t* planes = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) +
-                                                   route_ws_partials(sp, T, E));
-    split_planes_kernel<<<dim3(1024), dim3(256), 0, st>>>(centroids, (int64_t)E * H, planes);
-    router_logits_wide_kernel<<<dim3((unsigned)ceil_div(T, RW_TOK), (unsigned)sp.ks), dim3(512), 0,
-                                st>>>(static_cast<const uint16_t*>(x_bf16), T, H, planes, E,
-                                      sp.kper, part);
-  } else {
-    router_logits_kernel<<<dim3((unsigned)ceil_div(T, RT_TOK), (unsigned)ceil_div(E, RT_EXP),
-                                (unsigned)sp.ks),
-                           dim3(256), 0, st>>>(static_cast<const uint16_t*>(x_bf16), T, H,
-                                               centroids, E, sp.kper, part);
-  }
+  launch_logits(sp, x_bf16, T, H, centroids, E, workspace, part, st);
   // four tokens per workgroup per round; 1024 workgroups (four per CU at
   // 96 VGPRs: one round of residency) give a prefetching wave several tokens
   const int64_t sel_blocks = std::min<int64_t>(ceil_div(T, 4), 1024);
@@ -718,6 +735,38 @@ extern "C" int moe_route_scores(const void* x_bf16, int64_t T, int64_t H,
   MOE_INVALID(((uintptr_t)scores & 15) == 0, "moe_route_scores: scores must be 16-byte aligned");
   return route_impl(x_bf16, T, H, centroids, bias, E, n_group, topk_group, k, topk_idx, topk_w,
                     expert_counts, workspace, workspace_bytes, scores, score_sums, topk_s, stream);
+}
+
+extern "C" int moe_router_logits(const void* x_bf16, int64_t T, int64_t H, const float* centroids,
+                                 int32_t E, float* logits, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  clear_error();
+  MOE_INVALID(T >= 0, "moe_router_logits: T=%lld < 0", (long long)T);
+  MOE_INVALID(H > 0 && H % 128 == 0, "moe_router_logits: H=%lld must be a positive multiple of 128",
+              (long long)H);
+  MOE_INVALID(E >= 1, "moe_router_logits: E=%d < 1", (int)E);
+  MOE_UNSUPPORTED(E <= 1024, "moe_router_logits: E=%d > 1024 experts is not supported", (int)E);
+  MOE_UNSUPPORTED(T < (1ll << 31), "moe_router_logits: T=%lld is not supported", (long long)T);
+  if (T == 0) return MOE_OK;
+  MOE_INVALID(x_bf16 && centroids && logits, "moe_router_logits: null pointer");
+  MOE_INVALID(((uintptr_t)x_bf16 & 15) == 0 && ((uintptr_t)centroids & 15) == 0 &&
+                  ((uintptr_t)logits & 3) == 0,
+              "moe_router_logits: x and centroids must be 16-byte, logits 4-byte aligned");
+  const size_t need = moe_route_workspace_bytes(T, H, E);
+  MOE_REQUIRE(workspace != nullptr && workspace_bytes >= need && ((uintptr_t)workspace & 15) == 0,
+              MOE_ERR_WORKSPACE,
+              "moe_router_logits: workspace needs %zu bytes (16-byte aligned), got %zu", need,
+              workspace_bytes);
+  hipStream_t st = as_stream(stream);
+  const RouteSplit sp = route_split(T, H, E);
+  float* part = sp.ks == 1 ? logits : static_cast<float*>(workspace);
+  launch_logits(sp, x_bf16, T, H, centroids, E, workspace, part, st);
+  if (sp.ks > 1) {
+    const int64_t n = T * E;
+    sum_partials_kernel<<<dim3((unsigned)std::min<int64_t>(ceil_div(n, 256), 4096)), dim3(256), 0, st>>>(
+        part, (int)sp.ks, n, logits);
+  }
+  return check_launch("moe_router_logits");
 }
 
 extern "C" int moe_bias_update(const int32_t* expert_counts, float* bias, int32_t E, float gamma,

@@ -272,6 +272,25 @@ void dc_split(int64_t T, int64_t& slices, int64_t& slice) {
   slices = ceil_div(T, slice);
 }
 
+// dx and dC of given dlogit (kernels 2 to 4)
+void launch_dense_grads(const uint16_t* x, const float* centroids, const float* dlogit, int64_t T,
+                        int64_t H, int32_t E, const void* dx_in_bf16, void* dx_out_bf16,
+                        float* d_centroids, void* workspace, hipStream_t st) {
+  int64_t slices, slice;
+  dc_split(T, slices, slice);
+  dense_dx_kernel<<<dim3((unsigned)(H / DN), (unsigned)ceil_div(T, DM)), dim3(DT), 0, st>>>(
+      dlogit, centroids, static_cast<const uint16_t*>(dx_in_bf16), T, H, E,
+      static_cast<uint16_t*>(dx_out_bf16));
+  float* part = slices > 1 ? static_cast<float*>(workspace) : d_centroids;
+  dense_dc_kernel<<<dim3((unsigned)(H / DN), (unsigned)ceil_div(E, DM), (unsigned)slices), dim3(DT),
+                    0, st>>>(dlogit, x, T, H, E, slice, part);
+  if (slices > 1) {
+    const int64_t n4 = (int64_t)E * H / 4;
+    dc_reduce_kernel<<<dim3((unsigned)std::min<int64_t>(ceil_div(n4, DT), 4096)), dim3(DT), 0, st>>>(
+        part, n4, (int)slices, d_centroids);
+  }
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -315,8 +334,6 @@ extern "C" int moe_router_backward_dense(
                   ((uintptr_t)d_centroids & 15) == 0 && ((uintptr_t)dlogit & 15) == 0,
               "moe_router_backward_dense: x, centroids, scores, seq_f, dx_in, dx_out, d_centroids "
               "and dlogit must be 16-byte aligned");
-  int64_t slices, slice;
-  dc_split(T, slices, slice);
   const size_t need = moe_router_backward_dense_workspace_bytes(T, H, E);
   MOE_REQUIRE(need == 0 || (workspace != nullptr && workspace_bytes >= need &&
                             ((uintptr_t)workspace & 15) == 0),
@@ -327,16 +344,44 @@ extern "C" int moe_router_backward_dense(
   const uint16_t* x = static_cast<const uint16_t*>(x_bf16);
   dense_dlogit_kernel<<<dim3((unsigned)ceil_div(T, DT / 64)), dim3(DT), 0, st>>>(
       scores, score_sums, seq_f, topk_idx, d_topk_w, T, E, k, seq_len, alpha, dlogit);
-  dense_dx_kernel<<<dim3((unsigned)(H / DN), (unsigned)ceil_div(T, DM)), dim3(DT), 0, st>>>(
-      dlogit, centroids, static_cast<const uint16_t*>(dx_in_bf16), T, H, E,
-      static_cast<uint16_t*>(dx_out_bf16));
-  float* part = slices > 1 ? static_cast<float*>(workspace) : d_centroids;
-  dense_dc_kernel<<<dim3((unsigned)(H / DN), (unsigned)ceil_div(E, DM), (unsigned)slices), dim3(DT),
-                    0, st>>>(dlogit, x, T, H, E, slice, part);
-  if (slices > 1) {
-    const int64_t n4 = (int64_t)E * H / 4;
-    dc_reduce_kernel<<<dim3((unsigned)std::min<int64_t>(ceil_div(n4, DT), 4096)), dim3(DT), 0, st>>>(
-        part, n4, (int)slices, d_centroids);
-  }
+  launch_dense_grads(x, centroids, dlogit, T, H, E, dx_in_bf16, dx_out_bf16, d_centroids, workspace, st);
   return check_launch("moe_router_backward_dense");
+}
+
+extern "C" int moe_router_logits_backward(const void* x_bf16, const float* centroids,
+                                          const float* d_logits, int64_t T, int64_t H, int32_t E,
+                                          const void* dx_in_bf16, void* dx_out_bf16,
+                                          float* d_centroids, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
+  clear_error();
+  MOE_INVALID(T >= 0 && T < (1ll << 31), "moe_router_logits_backward: T=%lld out of range",
+              (long long)T);
+  MOE_INVALID(E >= 16 && E <= 1024 && E % 16 == 0,
+              "moe_router_logits_backward: E=%d must be a multiple of 16 in [16, 1024]", (int)E);
+  MOE_INVALID(H > 0 && H % 128 == 0,
+              "moe_router_logits_backward: H=%lld must be a positive multiple of 128", (long long)H);
+  MOE_INVALID(d_centroids && ((uintptr_t)d_centroids & 15) == 0,
+              "moe_router_logits_backward: d_centroids must be non-null and 16-byte aligned");
+  hipStream_t st = as_stream(stream);
+  if (T == 0) {
+    fill_f32_kernel<<<dim3(256), dim3(256), 0, st>>>(d_centroids, (int64_t)E * H, 0.0f);
+    return check_launch("moe_router_logits_backward(fill)");
+  }
+  MOE_INVALID(x_bf16 && centroids && d_logits && dx_out_bf16,
+              "moe_router_logits_backward: null pointer");
+  MOE_INVALID(dx_in_bf16 != dx_out_bf16, "moe_router_logits_backward: dx_in and dx_out alias");
+  MOE_INVALID(((uintptr_t)x_bf16 & 15) == 0 && ((uintptr_t)centroids & 15) == 0 &&
+                  ((uintptr_t)d_logits & 15) == 0 && ((uintptr_t)dx_in_bf16 & 15) == 0 &&
+                  ((uintptr_t)dx_out_bf16 & 15) == 0,
+              "moe_router_logits_backward: tensors must be 16-byte aligned");
+  const size_t need = moe_router_backward_dense_workspace_bytes(T, H, E);
+  MOE_REQUIRE(need == 0 || (workspace != nullptr && workspace_bytes >= need &&
+                            ((uintptr_t)workspace & 15) == 0),
+              MOE_ERR_WORKSPACE,
+              "moe_router_logits_backward: workspace needs %zu bytes (16-byte aligned), got %zu", need,
+              workspace_bytes);
+  MOE_UNSUPPORTED(ceil_div(T, DM) <= 65535, "moe_router_logits_backward: T too large");
+  launch_dense_grads(static_cast<const uint16_t*>(x_bf16), centroids, d_logits, T, H, E, dx_in_bf16,
+                     dx_out_bf16, d_centroids, workspace, st);
+  return check_launch("moe_router_logits_backward");
 }

@@ -48,6 +48,12 @@ extern "C" {
 #define MOE_ERR_HIP         -3  /* a HIP launch or API call failed            */
 #define MOE_ERR_WORKSPACE   -4  /* workspace too small                        */
 
+/* Element types and score functions of the gate (moe_gate). */
+#define MOE_TYPE_F32         0
+#define MOE_TYPE_BF16        1
+#define MOE_SCORE_SOFTMAX    0
+#define MOE_SCORE_SIGMOID    1
+
 /* Message of the last failed call on this thread ("" if none). */
 const char* moe_last_error(void);
 
@@ -576,6 +582,145 @@ int grouped_fp8_gemm_swiglu_keep(const uint8_t* A, const float* A_scale,
 int moe_combine(const void* expert_out_bf16, const int32_t* inv_perm,
                 const float* topk_w, const void* shared_out_bf16,
                 int64_t T, int32_t k, int64_t H, void* y_bf16, void* stream);
+
+/*
+ * moe_router_logits - the router's logits on their own: logits[t, e] = sum_h
+ * x[t, h] * centroids[e, h], the exact products summed in fp32 as moe_route
+ * sums them (its kernels), for a gate other than moe_route's (moe_gate).
+ * x_bf16 [T, H]; centroids [E, H] fp32; logits (out) [T, E] fp32; workspace:
+ * moe_route_workspace_bytes(T, H, E) bytes, 16-byte aligned.
+ * Requirements: H % 128 == 0, 1 <= E <= 1024; x and centroids 16-byte aligned.
+ * T == 0 is a no-op.
+ */
+int moe_router_logits(const void* x_bf16, int64_t T, int64_t H, const float* centroids, int32_t E,
+                      float* logits, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_router_logits_backward - the gradient of moe_router_logits, with the
+ * kernels of moe_router_backward_dense:
+ *   dx_out[t, :]      = bf16(dx_in[t, :] + sum_e d_logits[t, e] centroids[e, :])
+ *   d_centroids[e, :] = sum_t d_logits[t, e] x[t, :]    (fp32, fixed order)
+ * d_logits [T, E] fp32; dx_in_bf16 [T, H] or NULL (0), not aliasing dx_out;
+ * workspace: moe_router_backward_dense_workspace_bytes(T, H, E) bytes.
+ * Requirements: E % 16 == 0, 16 <= E <= 1024, H % 128 == 0; tensors 16-byte
+ * aligned.  T == 0 writes d_centroids = 0.
+ */
+int moe_router_logits_backward(const void* x_bf16, const float* centroids, const float* d_logits,
+                               int64_t T, int64_t H, int32_t E, const void* dx_in_bf16,
+                               void* dx_out_bf16, float* d_centroids, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * moe_gate - routing from given logits, in the forms moe_route does not have.
+ * For each token, with its logits l (fp32 or bf16; scores and weights in fp32):
+ *   s[e] = softmax(l)[e] over all E experts, or 1 / (1 + exp(-l[e]))
+ *   v[e] = s[e] + bias[e], or l[e] without a bias (the same order as s)
+ *   experts form n_group contiguous groups of E / n_group; a group's score is
+ *   its largest v (group_top 1) or the sum of its two largest s + bias
+ *   (group_top 2; of its only one, if it has one); the topk_group best groups
+ *   are kept (n_group 1: every expert is); the k largest v among the kept
+ *   experts are chosen; ties go to the lower index; ids are written in
+ *   ascending order;
+ *   w[j] = scale * s[e_j] / sum_j' s[e_j']  (renormalize 1; 0 if the sum is 0)
+ *          scale * s[e_j]                   (renormalize 0)
+ *   expert_counts[e] = number of tokens that chose e (overwritten).
+ * The choice is that of the exact s and v of the given logits and bias: where
+ * fp32 values are too close to be told apart they are formed in 64 bits.
+ * A logit of -inf excludes its expert: its score is 0 and it is chosen only
+ * where fewer than k others are kept, a row of nothing but -inf has weights 0;
+ * so does a bias of -inf, which leaves the score as it is.  Logits of +inf or
+ * NaN give unspecified scores and weights, and k different ids in [0, E).
+ *
+ * logits          [T, E] fp32 (logits_type MOE_TYPE_F32) or bf16 (MOE_TYPE_BF16)
+ * bias            [E] fp32, or NULL
+ * score           MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID
+ * topk_idx  (out) [T, k] int32, ascending per row;  topk_w (out) [T, k] fp32
+ * expert_counts (out) [E] int32
+ * scores    (out, optional: NULL skips it) [T, E] fp32: s
+ * Requirements: 1 <= E <= 1024; n_group <= 32 divides E; 1 <= topk_group <=
+ * n_group; group_top in {1, 2}; 1 <= k <= 8; k <= topk_group * E / n_group;
+ * scale finite; tensors aligned to their elements.
+ */
+int moe_gate(const void* logits, int32_t logits_type, int64_t T, int32_t E, const float* bias,
+             int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top, int32_t k,
+             int32_t renormalize, float scale, int32_t* topk_idx, float* topk_w,
+             int32_t* expert_counts, float* scores, void* stream);
+
+/*
+ * moe_gate_backward - gradient of moe_gate's weights, and of its scores, to the
+ * logits (the choice and the bias have none), in fp32:
+ *   ds[e]  = d_scores[t, e] (0 if NULL), and for every chosen e_j
+ *     renormalize 0:  ds[e_j] += scale * dw_j
+ *     renormalize 1:  ds[e_j] += scale * (dw_j - sum_i dw_i s_i / S) / S,
+ *                     S = sum_i s[e_i]  (nothing if S is 0)
+ *   d_logits[t, e] = s[e] * (ds[e] - sum_i ds[i] s[i])   (softmax)
+ *                    ds[e] * s[e] * (1 - s[e])            (sigmoid)
+ * logits, score, renormalize, scale as in moe_gate; topk_idx [T, k] its choice
+ * (an id outside [0, E) is passed over, its dw with it; an id named twice
+ * counts twice); d_topk_w [T, k]; d_scores [T, E] fp32 or NULL; d_logits (out)
+ * [T, E] in the logits' type, not aliasing them.  Requirements: 1 <= E <= 1024,
+ * 1 <= k <= 8, k <= E.
+ */
+int moe_gate_backward(const void* logits, int32_t logits_type, int64_t T, int32_t E, int32_t score,
+                      int32_t k, int32_t renormalize, float scale, const int32_t* topk_idx,
+                      const float* d_topk_w, const float* d_scores, void* d_logits, void* stream);
+
+/*
+ * int8_quant_rows - activations to 8-bit integers, one scale a token:
+ *   scales[m] = max_k |in[m, k]| * (1 / 127)  (both fp32, the product rounded
+ *               once: within 2^-23 of the quotient; 1 if it is 0)
+ *   out[m, k] = in[m, k] / scales[m], the exact quotient rounded to the nearest
+ *               whole number, ties to even: -127 .. 127
+ * in_bf16 [M, ld_in], K columns used (16-byte aligned); out_int8 (out) [M, K]
+ * (8-byte aligned); scales (out) [M] fp32.
+ * Requirements: K % 8 == 0, K <= 2^24, ld_in % 8 == 0, ld_in >= K.
+ */
+int int8_quant_rows(const void* in_bf16, int64_t M, int64_t K, int64_t ld_in, int8_t* out_int8,
+                    float* scales, void* stream);
+
+/*
+ * int8_quant_channels - weights to 8-bit integers, one scale an output channel:
+ * the rule of int8_quant_rows on each row of w_f32 [G, N, K] fp32 (16-byte
+ * aligned); out_int8 (out) [G, N, K] (8-byte aligned); scales (out) [G, N].
+ * Requirements: K % 8 == 0, K <= 2^24, N > 0, G * N < 2^31.  G == 0 is a no-op.
+ */
+int int8_quant_channels(const float* w_f32, int64_t G, int64_t N, int64_t K, int8_t* out_int8,
+                        float* scales, void* stream);
+
+/*
+ * grouped_int8_gemm - grouped product of 8-bit integers with a scale for each
+ * token and each output channel (G = 1: a linear layer).  For group g, rows r
+ * in [group_offsets[g], group_offsets[g+1]):
+ *   C[r, n] = bf16( sum_k A[src, k] * B[g, n, k] * (A_scale[src] * B_scale[g, n]) )
+ * src = a_row_index[r] if that is not NULL, else r.  The sum is exact (32-bit
+ * integers), converted to fp32 once and scaled in fp32.
+ *
+ * A        [A_rows, K] int8;  A_scale [A_rows] fp32
+ * a_row_index [M_total] int32 or NULL, A_rows: as in grouped_fp8_gemm
+ * B        [G, N, K] int8 (K contiguous);  B_scale [G, N] fp32
+ * group_offsets [G+1] int32 on the device, non-decreasing, [0] == 0, [G] <=
+ *          M_total; rows from [G] on are left as they were
+ * C  (out) [M_total, N] bf16
+ * Requirements: N % 8 == 0, N <= 2^21, K % 16 == 0, K < 2^17, 1 <= G <= 1024;
+ * A, B, C 16-byte aligned.
+ */
+int grouped_int8_gemm(const int8_t* A, const float* A_scale, const int32_t* a_row_index,
+                      int64_t A_rows, const int8_t* B, const float* B_scale,
+                      const int32_t* group_offsets, int32_t G, int64_t M_total, int64_t N, int64_t K,
+                      void* C_bf16, void* stream);
+
+/*
+ * grouped_int8_gemm_swiglu - the gate+up product with SwiGLU in its epilogue.
+ * B holds each group's fused weight [2I, K]: rows [0, I) gate, [I, 2I) up.
+ * With gt and ut the fp32 values that grouped_int8_gemm (N = 2I) rounds to C:
+ *   H[r, c] = bf16( gt / (1 + exp(-gt)) * ut )   (fp32)
+ * H_bf16 (out) [M_total, I]; B_scale [G, 2I]; the rest and the requirements as
+ * grouped_int8_gemm's, for I in place of N.
+ */
+int grouped_int8_gemm_swiglu(const int8_t* A, const float* A_scale, const int32_t* a_row_index,
+                             int64_t A_rows, const int8_t* B, const float* B_scale,
+                             const int32_t* group_offsets, int32_t G, int64_t M_total, int64_t I,
+                             int64_t K, void* H_bf16, void* stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */

@@ -23,10 +23,13 @@ What each module computes, and the passage it follows:
 * ``swiglu``   - SwiGLU + requantisation (the pages are silent on the expert
   FFN form; SwiGLU is the workload definition).
 * ``combine``  - weighted combine plus the shared expert.
+* ``gate``     - the gate on given logits (softmax or sigmoid scores) and its
+  gradient; the formulas of include/moe_fp8.h.
+* ``int8``     - quantisation by rows and the grouped product in 8-bit integers.
 * ``layer``    - the whole forward, and a per-token direct form used as a pin.
 
 Parity pins: every function here is pinned in ``tests/test_oracle_*.py``.
 Parity unpinned by the pages: the pages print no worked example, so every
 pin is a closed form, an invariant, a brute force or a library cross-check.
 """
-from . import formats, quant, route, balance, permute, gemm, swiglu, combine, layer  # noqa: F401
+from . import formats, quant, route, balance, permute, gemm, swiglu, combine, gate, int8, layer  # noqa: F401

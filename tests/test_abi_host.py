@@ -248,3 +248,81 @@ def test_workspace_sizes():
     assert L.moe_route_workspace_bytes(16384, 7168, 256) == 4 * 16384 * 256 * 4 + 3 * 256 * 7168 * 2
     b = L.moe_route_workspace_bytes(128, 7168, 256)
     assert b % (128 * 256 * 4) == 0 and b >= 128 * 256 * 4
+
+
+def test_gate_validation():
+    def g(lt=0, T=4, E=64, score=0, ng=4, tg=2, gt=2, k=4, rn=1, scale=1.0, logits=FAKE, idx=FAKE,
+          counts=FAKE, scores=None, bias=None):
+        return rc("moe_gate", logits, lt, T, E, bias, score, ng, tg, gt, k, rn, scale, idx, FAKE, counts,
+                  scores, None)
+    assert g(T=-1) == L.MOE_ERR_INVALID and "T=-1" in L.last_error()
+    assert g(E=0) == L.MOE_ERR_INVALID and g(E=66) == L.MOE_ERR_INVALID and "n_group" in L.last_error()
+    assert g(E=1028, k=1) == L.MOE_ERR_UNSUPPORTED and "1024" in L.last_error()
+    assert g(lt=2) == L.MOE_ERR_INVALID and g(score=2) == L.MOE_ERR_INVALID and g(rn=2) == L.MOE_ERR_INVALID
+    assert g(tg=5) == L.MOE_ERR_INVALID and g(tg=0) == L.MOE_ERR_INVALID
+    assert g(gt=3) == L.MOE_ERR_INVALID and "group_top=3" in L.last_error()
+    assert g(k=0) == L.MOE_ERR_INVALID and g(k=9) == L.MOE_ERR_UNSUPPORTED
+    assert g(E=8, k=5) == L.MOE_ERR_INVALID        # two groups of two are kept
+    assert g(E=66, ng=33, tg=33) == L.MOE_ERR_UNSUPPORTED and "n_group=33" in L.last_error()
+    assert g(scale=float("inf")) == L.MOE_ERR_INVALID and g(scale=float("nan")) == L.MOE_ERR_INVALID
+    assert g(logits=None) == L.MOE_ERR_INVALID and g(idx=None) == L.MOE_ERR_INVALID
+    assert g(counts=None) == L.MOE_ERR_INVALID and "expert_counts" in L.last_error()
+    assert g(logits=ctypes.c_void_p(4098)) == L.MOE_ERR_INVALID and "aligned" in L.last_error()
+    assert g(scores=ctypes.c_void_p(4098)) == L.MOE_ERR_INVALID
+    assert g(bias=ctypes.c_void_p(4097)) == L.MOE_ERR_INVALID
+
+    def b(lt=0, T=4, E=64, score=0, k=4, rn=1, scale=1.0, idx=FAKE, dl=ctypes.c_void_p(8192), ds=None):
+        return rc("moe_gate_backward", FAKE, lt, T, E, score, k, rn, scale, idx, FAKE, ds, dl, None)
+    assert b(k=9) == L.MOE_ERR_UNSUPPORTED and b(E=3) == L.MOE_ERR_INVALID and b(E=2000) == L.MOE_ERR_UNSUPPORTED
+    assert b(idx=None) == L.MOE_ERR_INVALID and b(dl=None) == L.MOE_ERR_INVALID
+    assert b(dl=FAKE) == L.MOE_ERR_INVALID and "alias" in L.last_error()
+    assert b(ds=ctypes.c_void_p(4098)) == L.MOE_ERR_INVALID and "aligned" in L.last_error()
+    assert b(rn=-1) == L.MOE_ERR_INVALID and b(scale=float("nan")) == L.MOE_ERR_INVALID
+    assert b(T=0, idx=None, dl=None) == L.MOE_OK
+
+
+def test_router_logits_validation():
+    def f(T=4, H=256, E=16, x=FAKE, out=FAKE, ws=FAKE, n=1 << 20):
+        return rc("moe_router_logits", x, T, H, FAKE, E, out, ws, n, None)
+    assert f(H=100) == L.MOE_ERR_INVALID and f(E=0) == L.MOE_ERR_INVALID and f(T=-1) == L.MOE_ERR_INVALID
+    assert f(E=1025) == L.MOE_ERR_UNSUPPORTED
+    assert f(x=None) == L.MOE_ERR_INVALID and f(x=ctypes.c_void_p(4104)) == L.MOE_ERR_INVALID
+    assert f(n=4) == L.MOE_ERR_WORKSPACE and f(ws=None) == L.MOE_ERR_WORKSPACE
+    assert f(T=0, x=None, out=None) == L.MOE_OK
+
+    def b(T=4, H=256, E=16, dx=ctypes.c_void_p(8192), dxin=None, dC=FAKE, ws=FAKE, n=1 << 30):
+        return rc("moe_router_logits_backward", FAKE, FAKE, FAKE, T, H, E, dxin, dx, dC, ws, n, None)
+    assert b(E=24) == L.MOE_ERR_INVALID and b(E=1040) == L.MOE_ERR_INVALID and b(H=64) == L.MOE_ERR_INVALID
+    assert b(dC=None) == L.MOE_ERR_INVALID and b(dx=None) == L.MOE_ERR_INVALID
+    assert b(dx=FAKE, dxin=FAKE) == L.MOE_ERR_INVALID and "alias" in L.last_error()
+    assert b(T=5000, n=16) == L.MOE_ERR_WORKSPACE
+
+
+def test_int8_validation():
+    def q(M=4, K=128, ld=128, x=FAKE, out=FAKE):
+        return rc("int8_quant_rows", x, M, K, ld, out, FAKE, None)
+    assert q(K=100) == L.MOE_ERR_INVALID and "K=100" in L.last_error()
+    assert q(ld=120) == L.MOE_ERR_INVALID and q(ld=132) == L.MOE_ERR_INVALID and q(M=-1) == L.MOE_ERR_INVALID
+    assert q(x=None) == L.MOE_ERR_INVALID and q(x=ctypes.c_void_p(4104)) == L.MOE_ERR_INVALID
+    assert q(out=ctypes.c_void_p(4100)) == L.MOE_ERR_INVALID and "aligned" in L.last_error()
+    assert q(K=1 << 25, ld=1 << 25) == L.MOE_ERR_UNSUPPORTED
+    assert q(M=0, x=None, out=None) == L.MOE_OK
+
+    def c(G=2, N=4, K=128, w=FAKE):
+        return rc("int8_quant_channels", w, G, N, K, FAKE, FAKE, None)
+    assert c(K=12) == L.MOE_ERR_INVALID and c(N=0) == L.MOE_ERR_INVALID and c(G=-1) == L.MOE_ERR_INVALID
+    assert c(G=1 << 20, N=1 << 12) == L.MOE_ERR_UNSUPPORTED and c(w=None) == L.MOE_ERR_INVALID
+    assert c(G=0, w=None) == L.MOE_OK
+
+    for name in ("grouped_int8_gemm", "grouped_int8_gemm_swiglu"):
+        def g(G=4, M=100, N=128, K=256, rows=100, idx=None, a=FAKE, out=FAKE):
+            return rc(name, a, FAKE, idx, rows, FAKE, FAKE, FAKE, G, M, N, K, out, None)
+        assert g(N=100) == L.MOE_ERR_INVALID and "=100" in L.last_error() and name in L.last_error()
+        assert g(K=24) == L.MOE_ERR_INVALID and g(K=0) == L.MOE_ERR_INVALID and g(N=0) == L.MOE_ERR_INVALID
+        assert g(K=131072) == L.MOE_ERR_UNSUPPORTED and g(G=1025) == L.MOE_ERR_UNSUPPORTED
+        assert g(G=0) == L.MOE_ERR_INVALID and g(M=-1) == L.MOE_ERR_INVALID
+        assert g(rows=99) == L.MOE_ERR_INVALID and "A_rows" in L.last_error()
+        assert g(rows=0, idx=FAKE) == L.MOE_ERR_INVALID
+        assert g(a=None) == L.MOE_ERR_INVALID and g(out=None) == L.MOE_ERR_INVALID
+        assert g(a=ctypes.c_void_p(4104)) == L.MOE_ERR_INVALID and "aligned" in L.last_error()
+        assert g(M=0, a=None, out=None) == L.MOE_OK
