@@ -6,12 +6,11 @@
 //
 // The sum is exact in 32 bits (K < 2^17 codes of at most 2^7 in size), so the
 // order of the products does not matter; it is rounded to fp32 once.
-#include "common.h"
+#include "int8_common.h"
 
 namespace moe {
+namespace int8 {
 namespace {
-
-typedef int v4i __attribute__((ext_vector_type(4)));
 
 constexpr int T8 = 256;     // threads: four waves
 constexpr int BM8 = 64;     // rows of a tile, 16 to a wave
@@ -19,21 +18,8 @@ constexpr int BN8 = 64;     // output columns of a tile
 constexpr int KB8 = 64;     // bytes of K a step
 constexpr int P8 = KB8 + 16;
 
-struct Int8Args {
-  const int8_t* A;
-  const float* sa;
-  const int32_t* index;
-  int64_t A_rows;
-  const int8_t* B;
-  const float* sb;
-  const int32_t* offs;
-  int G;
-  int64_t M_total, N, K;  // N: columns of the output (B has N, or 2N with SwiGLU)
-  uint16_t* C;
-};
-
 // The group and first row of the m-th row tile; false past the last.
-__device__ __forceinline__ bool find_tile(const Int8Args& a, int64_t m, int* g, int* r0, int* r1) {
+__device__ __forceinline__ bool find_tile(const Args& a, int64_t m, int* g, int* r0, int* r1) {
   const int lane = threadIdx.x & 63;
   int64_t before = 0;
   for (int g0 = 0; g0 < a.G; g0 += 64) {
@@ -62,14 +48,14 @@ __device__ __forceinline__ bool find_tile(const Int8Args& a, int64_t m, int* g, 
 }
 
 template <bool SWIGLU>
-__global__ __launch_bounds__(T8) void int8_tile_kernel(Int8Args a) {
+__global__ __launch_bounds__(T8) void int8_tile_kernel(Args a) {
   constexpr int NB = SWIGLU ? 2 : 1;
   __shared__ __attribute__((aligned(16))) int8_t sA[BM8][P8];
   __shared__ __attribute__((aligned(16))) int8_t sB[NB * BN8][P8];
-  int g, r0, r1;
-  if (!find_tile(a, blockIdx.y, &g, &r0, &r1)) return;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int64_t n0 = (int64_t)blockIdx.x * BN8;
+  int g, r0, r1;
+  for (int64_t m = blockIdx.y; find_tile(a, m, &g, &r0, &r1); m += gridDim.y) {
   // copies: thread -> row tid / 4, 16 bytes (tid % 4)
   const int cr = tid >> 2, cc = (tid & 3) * 16;
   int64_t arow = min(r0 + cr, r1 - 1);
@@ -116,12 +102,10 @@ __global__ __launch_bounds__(T8) void int8_tile_kernel(Int8Args a) {
       const int64_t n = n0 + 16 * j + (lane & 15);
       if (n >= a.N) continue;
       float v = (float)acc[0][j][r] * (s * sb[n]);
-      if (SWIGLU) {
-        const float u = (float)acc[NB - 1][j][r] * (s * sb[a.N + n]);
-        v = v / (1.0f + expf(-v)) * u;
-      }
+      if (SWIGLU) v = silu_mul(v, (float)acc[NB - 1][j][r] * (s * sb[a.N + n]));
       a.C[(int64_t)row * a.N + n] = (uint16_t)f32_to_bf16_rne(v);
     }
+  }
   }
 }
 
@@ -147,20 +131,22 @@ int int8_gemm(const char* who, bool swiglu, const int8_t* A, const float* A_scal
                   ((uintptr_t)A_scale & 3) == 0 && ((uintptr_t)B_scale & 3) == 0 &&
                   ((uintptr_t)a_row_index & 3) == 0 && ((uintptr_t)group_offsets & 3) == 0,
               "%s: A, B and the output must be 16-byte aligned, scales and indices 4-byte", who);
-  const Int8Args a{A, A_scale, a_row_index, A_rows, B, B_scale, group_offsets, G, M_total, N, K,
+  const Args a{A, A_scale, a_row_index, A_rows, B, B_scale, group_offsets, G, M_total, N, K,
                    static_cast<uint16_t*>(C)};
-  const int64_t mtiles = std::min<int64_t>(M_total, G + M_total / BM8);
+  const int64_t mtiles = std::min<int64_t>({M_total, G + M_total / BM8, 65535});
   const dim3 grid((unsigned)ceil_div(N, BN8), (unsigned)mtiles);
-  MOE_UNSUPPORTED(mtiles <= 65535, "%s: M_total=%lld is not supported", who, (long long)M_total);
-  if (swiglu) int8_tile_kernel<true><<<grid, dim3(T8), 0, st>>>(a);
+  if (M_total / G >= 32 && K > 128 && (!a_row_index || A_rows * K < 0xFFF00000ll)) launch_wide(a, swiglu, st);
+  else if (swiglu) int8_tile_kernel<true><<<grid, dim3(T8), 0, st>>>(a);
   else int8_tile_kernel<false><<<grid, dim3(T8), 0, st>>>(a);
   return check_launch(who);
 }
 
 }  // namespace
+}  // namespace int8
 }  // namespace moe
 
 using namespace moe;
+using namespace moe::int8;
 
 extern "C" int grouped_int8_gemm(const int8_t* A, const float* A_scale, const int32_t* a_row_index,
                                  int64_t A_rows, const int8_t* B, const float* B_scale,
