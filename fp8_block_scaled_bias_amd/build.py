@@ -32,6 +32,16 @@ FLAGS = [
     "-mllvm", "-amdgpu-mfma-vgpr-form",
     "-I", INCLUDE, "-I", CSRC,
 ]
+# the int8 tile kernel keeps its accumulators in AGPRs: one wave a SIMD with
+# all 512 registers
+AGPR_FORM = {"int8_wide.hip"}
+
+
+def flags(src):
+    if os.path.basename(src) not in AGPR_FORM:
+        return FLAGS
+    i = FLAGS.index("-amdgpu-mfma-vgpr-form")
+    return FLAGS[:i - 1] + FLAGS[i + 1:]
 
 
 def _run(cmd):
@@ -56,7 +66,7 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
 
     def compile_one(pair):
         src, obj = pair
-        out = _run([HIPCC, *FLAGS, "-c", src, "-o", obj])
+        out = _run([HIPCC, *flags(src), "-c", src, "-o", obj])
         if verbose and out.strip():
             print(out)
         return obj
