@@ -22,8 +22,11 @@
 //  * Copies run on across tiles: the next tile's first two K blocks load
 //    while the last ones of this tile are multiplied.
 //  * Persistent workgroups; those of an XCD (blockIdx % 8) share a contiguous
-//    range of tiles, M tiles of one weight panel next to each other, so they
-//    share its L2.
+//    range of tiles.  A group's tiles are numbered in strips of 8 M tiles, N
+//    tile by N tile, so that the 32 tiles at work on an XCD read 8 row and 4
+//    weight panels through its L2.
+//  * The epilogue runs between MFMAs too: A0's results while the last K block
+//    works on A1, A1's while the next tile's first works on A0.
 // Every copy goes through a buffer resource over the rows it may touch; lanes
 // with nothing to read (rows past a tile's end, the last K block past a row's
 // end) have an offset outside it, and what their slots hold is not used: such
@@ -42,6 +45,7 @@ using gemm::swz;
 constexpr int WT = 256;
 constexpr int REG = 128 * 128;      // a region: 128 rows x 128 B
 constexpr int STAGE = 4 * REG;      // A0, A1, B0, B1
+constexpr int STRIP = 8;            // M tiles of a strip
 constexpr int OFF_OUT = 2 * STAGE;  // per wave 32 rows x 64 B
 constexpr int OFF_PREF = OFF_OUT + 4 * 2048;
 constexpr int OFF_OFFS = OFF_PREF + 4112;
@@ -118,11 +122,12 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
     gh = g = __builtin_amdgcn_readfirstlane(g);
     const uint32_t cnt = (uint32_t)(s_pref[g + 1] - s_pref[g]);
     const uint32_t rem = (uint32_t)(L - (int64_t)s_pref[g] * ntiles);
-    const uint32_t nt = rem / cnt;
+    const uint32_t strip = rem / (STRIP * (uint32_t)ntiles), r2 = rem - strip * (STRIP * (uint32_t)ntiles);
+    const uint32_t w = min((uint32_t)STRIP, cnt - strip * STRIP), nt = r2 / w;
     Tile t;
     t.g = g;
     t.n0 = __builtin_amdgcn_readfirstlane((int)(nt * TN));
-    t.m0 = __builtin_amdgcn_readfirstlane(s_offs[g] + (int)(rem - nt * cnt) * 256);
+    t.m0 = __builtin_amdgcn_readfirstlane(s_offs[g] + (int)(strip * STRIP + r2 - nt * w) * 256);
     t.rows = __builtin_amdgcn_readfirstlane(min(256, s_offs[g + 1] - t.m0));
     return t;
   };
@@ -172,12 +177,14 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
     }
     if (GATHER) {
       ra = rsrc(a.A, (uint32_t)a.A_rows * K);
+      // (the lane's place passes through an empty asm so that what follows
+      // is computed here and not kept in registers over the K loop)
+      int ln = lane;
+      asm volatile("" : "+v"(ln));
 #pragma unroll
       for (int p = 0; p < 8; ++p) {
-        const int row = 128 * (p >> 2) + crow(p & 3);
-        va[p] = row < t.rows
-                    ? index_of(co, row) * K + (uint32_t)(((lane & 7) ^ swz(row)) << 4)
-                    : kOut;
+        const int row = 128 * (p >> 2) + 32 * wv + 8 * (p & 3) + (ln >> 3);
+        va[p] = row < t.rows ? index_of(co, row) * K + (uint32_t)(((ln & 7) ^ swz(row)) << 4) : kOut;
       }
       int g2 = cg;
       index_copy(tile_at(g2, co + 1), co + 1);
@@ -237,76 +244,114 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
   auto scale_copy = [&]() {  // its scales: rows and columns 64 wv .. +63
     const uint32_t m = (uint32_t)__builtin_amdgcn_readfirstlane(
         (int)(lds0 + OFF_SC + (to & 1) * 2048 + wv * 256));
-    const int row = 64 * wv + lane;
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    const int row = 64 * wv + ln;
     if (GATHER)
       copy4(rsrc(a.sa, (uint32_t)a.A_rows * 4), row < t.rows ? index_of(to, row) * 4 : kOut, m);
     else
       copy4(rsrc(a.sa + t.m0, (uint32_t)t.rows * 4), (uint32_t)row * 4, m);
     const int h = wv >> 1;
     copy4(rsrc(a.sb + (int64_t)t.g * b_rows + t.n0 + h * b_half, (uint32_t)cols_of(t, h) * 4),
-          (uint32_t)(64 * (wv & 1) + lane) * 4, m + 1024);
+          (uint32_t)(64 * (wv & 1) + ln) * 4, m + 1024);
   };
 
-  // Results of block (i, j) of A half H and B half B (SwiGLU: of both): lane
-  // (q, l32) holds token row l32 and the columns 8 g + 4 q .. +3 (g = 0..3).
-  // Through the wave's own 2 KB of LDS (16-byte chunk c of row r in slot c ^
-  // (r / 2) % 4) into rows of 64 bytes.  The fp32 result is rounded once, to
-  // bf16.
-  auto emit = [&](auto H_, auto B_, auto I_, auto J_) __attribute__((always_inline)) {
-    constexpr int H = decltype(H_)::value, B = decltype(B_)::value;
-    constexpr int i = decltype(I_)::value, j = decltype(J_)::value;
-    const int row0 = 128 * H + 64 * i + 32 * wm;
-    if (row0 >= t.rows) return;
-    // the lane's place passes through an empty asm so that the addresses below
-    // are formed here and not kept in registers over the K loop
-    int ln = lane;
-    asm volatile("" : "+v"(ln));
-    const int l32 = ln & 31, q = ln >> 5;
-    const float* sc = reinterpret_cast<const float*>(smem + OFF_SC + (to & 1) * 2048);
-    uint8_t* out = smem + OFF_OUT + wv * 2048;
-    const __amdgpu_buffer_rsrc_t rc = __builtin_amdgcn_make_buffer_rsrc(
-        a.C + (int64_t)t.m0 * N, 0, (int)((uint32_t)t.rows * (uint32_t)N * 2), 0x00020000);
-    const float sa = sc[row0 + l32];
+  // ---- epilogue.  Lane (q, l32) holds token row l32 of a block (i, j) of A
+  // half H and B half B (SwiGLU: gate in B0, up in B1) and its columns 8 g +
+  // 4 q .. +3 (g = 0..3).  They go through the wave's own 2 KB of LDS (16-byte
+  // chunk c of row r in slot c ^ (r / 2) % 4) into rows of 64 bytes.  The fp32
+  // result is rounded once, to bf16.  Blocks are taken in the order E = 0 ..
+  // NE-1.  Every block is stored, rows and columns past the tile's end to
+  // offsets that the hardware drops, so that a phase always issues the same
+  // number of stores.
+  constexpr int NE = SWIGLU ? 4 : 8;  // blocks of a half
+  typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+  struct Done {
+    Tile t;
+    int slot;  // of its scales
+  };
+  // lane parts of the epilogue's addresses: the scales of a row block and of 4
+  // columns, its own rows of LDS written and read, the output
+  const uint32_t e_row = OFF_SC + (32 * wm + l32) * 4, e_col = OFF_SC + 1024 + (32 * wn + 4 * q) * 4;
+  const uint32_t e_wr = OFF_OUT + wv * 2048 + l32 * 64 + (((l32 >> 1) & 3) << 4) + 8 * q;
+  const uint32_t e_rd = OFF_OUT + wv * 2048 + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+  const uint32_t e_lcol = 32 * wn + 8 * (lane & 3);
+  const uint32_t e_st = ((32 * wm + (lane >> 2)) * (uint32_t)N + e_lcol) * 2;
+  // Scales of the 8 results of a slot: gate and up columns of one g with
+  // SwiGLU, the columns of two g without; read a slot ahead.
+  struct Scales {
+    float row;
+    float4 col[2];
+  };
+  auto emit_scales = [&](auto H_, auto S_, const Done& d, Scales& e) __attribute__((always_inline)) {
+    constexpr int H = decltype(H_)::value, S = decltype(S_)::value;  // slot 0..15 of a half
+    constexpr int per = 16 / NE, E = S / per;
+    constexpr int B = E >> 2, i = (E >> 1) & 1, j = E & 1, g = SWIGLU ? S % 4 : 2 * (S % 2);
+    const uint8_t* base = smem + d.slot * 2048;
+    e.row = *reinterpret_cast<const float*>(base + e_row + (128 * H + 64 * i) * 4);
+    const uint8_t* c = base + e_col + (128 * B + 64 * j + 8 * g) * 4;
+    e.col[0] = *reinterpret_cast<const float4*>(c);
+    e.col[1] = *reinterpret_cast<const float4*>(c + (SWIGLU ? 128 : 8) * 4);
+  };
+  auto emit_math = [&](auto H_, auto S_, const Scales& e) __attribute__((always_inline)) {
+    constexpr int H = decltype(H_)::value, S = decltype(S_)::value;
+    constexpr int per = 16 / NE, E = S / per;
+    constexpr int B = E >> 2, i = (E >> 1) & 1, j = E & 1, g = SWIGLU ? S % 4 : 2 * (S % 2);
+    float v[2][4];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int c = 64 * j + 32 * wn + 8 * g + 4 * q;  // column of its half
-      const float4 s0 = *reinterpret_cast<const float4*>(sc + 256 + 128 * B + c);
-      const float w0[4] = {s0.x, s0.y, s0.z, s0.w};
-      float v[4];
+    for (int h = 0; h < 2; ++h) {
+      const float w[4] = {e.col[h].x, e.col[h].y, e.col[h].z, e.col[h].w};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = (float)acc[H][B][i][j][4 * g + r] * (sa * w0[r]);
-      if (SWIGLU) {
-        const float4 s1 = *reinterpret_cast<const float4*>(sc + 256 + 128 + c);
-        const float w1[4] = {s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = silu_mul(v[r], (float)acc[H][1][i][j][4 * g + r] * (sa * w1[r]));
-      }
-      *reinterpret_cast<uint2*>(out + l32 * 64 + ((g ^ ((l32 >> 1) & 3)) << 4) + 8 * q) =
-          make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
-      __builtin_amdgcn_sched_barrier(0);
+      for (int r = 0; r < 4; ++r)
+        v[h][r] = (float)(SWIGLU ? acc[H][h][i][j][4 * g + r] : acc[H][B][i][j][4 * (g + h) + r]) * (e.row * w[r]);
     }
-    const int col = t.n0 + 128 * B + 64 * j + 32 * wn + 8 * (ln & 3);
+    if (SWIGLU) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[0][r] = silu_mul(v[0][r], v[1][r]);
+    }
+#pragma unroll
+    for (int h = 0; h < (SWIGLU ? 1 : 2); ++h)
+      *reinterpret_cast<uint2*>(smem + (e_wr ^ ((g + h) << 4))) =
+          make_uint2(f32x2_to_bf16x2(v[h][0], v[h][1]), f32x2_to_bf16x2(v[h][2], v[h][3]));
+  };
+  auto emit_read = [&](v4u (&w)[2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) w[r] = *reinterpret_cast<const v4u*>(smem + e_rd + r * 1024);
+  };
+  // (a resource from the block's first row and column to the tile's last row:
+  // offsets of rows past it are outside; columns past N are put outside)
+  auto emit_store = [&](auto H_, auto E_, const v4u (&w)[2], const Done& d) __attribute__((always_inline)) {
+    constexpr int H = decltype(H_)::value, E = decltype(E_)::value;
+    constexpr int B = E >> 2, i = (E >> 1) & 1, j = E & 1;
+    const uint32_t c0 = (uint32_t)d.t.n0 + 128 * B + 64 * j;
+    const uint32_t off = e_st | (c0 + e_lcol < (uint32_t)N ? 0u : kOut);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int row = 16 * r + (ln >> 2);
-      const uint4 d = *reinterpret_cast<const uint4*>(out + row * 64 + (((ln & 3) ^ ((row >> 1) & 3)) << 4));
-      typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-      const v4u w = {d.x, d.y, d.z, d.w};
-      if (col < N)
-        __builtin_amdgcn_raw_buffer_store_b128(w, rc, ((row0 + row) * (int)N + col) * 2, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
+      const int r0 = 128 * H + 64 * i + 16 * r;
+      const int bytes = max(0, (d.t.rows - r0) * (int)N - (int)c0) * 2;
+      __builtin_amdgcn_raw_buffer_store_b128(
+          w[r], __builtin_amdgcn_make_buffer_rsrc(a.C + (int64_t)(d.t.m0 + r0) * N + c0, 0, bytes, 0x00020000),
+          off, 0, 0);
     }
   };
-  auto emit_half = [&](auto H_) __attribute__((always_inline)) {
-    emit(H_, ic<0>(), ic<0>(), ic<0>());
-    emit(H_, ic<0>(), ic<0>(), ic<1>());
-    emit(H_, ic<0>(), ic<1>(), ic<0>());
-    emit(H_, ic<0>(), ic<1>(), ic<1>());
-    if (!SWIGLU) {
-      emit(H_, ic<1>(), ic<0>(), ic<0>());
-      emit(H_, ic<1>(), ic<0>(), ic<1>());
-      emit(H_, ic<1>(), ic<1>(), ic<0>());
-      emit(H_, ic<1>(), ic<1>(), ic<1>());
+  // slot n (0..7) of the first (PART 0) or second (1) phase of a half's epilogue
+  Scales es;
+  auto emit_slot = [&](auto H_, auto PART_, auto N_, const Done& d) __attribute__((always_inline)) {
+    constexpr int PART = decltype(PART_)::value, n = decltype(N_)::value, S = 8 * PART + n;
+    constexpr int per = 16 / NE;  // slots of a block
+    constexpr int E = S / per, part = S % per;
+    constexpr bool stores = part == 0 && E > 0;
+    v4u w[2];
+    if (S == 0) emit_scales(H_, ic<0>(), d, es);
+    if (stores) emit_read(w);
+    Scales next;
+    if (S < 15) emit_scales(H_, ic<(S < 15 ? S + 1 : 0)>(), d, next);
+    emit_math(H_, ic<S>(), es);
+    es = next;
+    if (stores) emit_store(H_, ic<(stores ? E - 1 : 0)>(), w, d);
+    if (S == 15) {
+      emit_read(w);
+      emit_store(H_, ic<NE - 1>(), w, d);
     }
   };
 
@@ -340,61 +385,83 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
   barrier();
 
   // A phase: MFMAs of A half H and B half B; reads region R of stage rst for
-  // the next one, copies region CR into stage cst.  FIRST: from zero.
-  // LIVE: with MFMAs (a tile of at most 128 rows has none for A1).
+  // the next one (early, so that the wait at its end finds them done), copies
+  // region CR into stage cst.  FIRST: from zero.  PART 0, 1: part of the
+  // epilogue of the other half of d.  W: the wait that ends the phase.
   auto phase = [&](auto H_, auto B_, auto R_, uint32_t rst, auto CR_, uint32_t cst, auto FIRST_,
-                   auto LIVE_) __attribute__((always_inline)) {
+                   auto PART_, auto W_, const Done& d) __attribute__((always_inline)) {
     constexpr int H = decltype(H_)::value, B = decltype(B_)::value;
     constexpr bool FIRST = decltype(FIRST_)::value;
+    auto slot = [&](auto N_) __attribute__((always_inline)) {
+      constexpr int n = decltype(N_)::value;
+      constexpr int i = n >> 2, ks = n & 3;  // block of A, K chunk
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {  // block i of A, K chunk ks
-      const int i = n >> 2, ks = n & 3;
-      if (decltype(LIVE_)::value) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const v16i zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-          acc[H][B][i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
-              fr[2 + B][j][ks], fr[H][i][ks], FIRST && ks == 0 ? zero : acc[H][B][i][j], 0, 0, 0);
-        }
+      for (int j = 0; j < 2; ++j) {
+        const v16i zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+        acc[H][B][i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
+            fr[2 + B][j][ks], fr[H][i][ks], FIRST && ks == 0 ? zero : acc[H][B][i][j], 0, 0, 0);
       }
-      read_one(R_, n, rst);
-      if (n == 1) copy_rows(CR_, ic<0>(), cst);
-      if (n == 3) copy_rows(CR_, ic<1>(), cst);
-      if (n == 5) copy_rows(CR_, ic<2>(), cst);
-      if (n == 7) copy_rows(CR_, ic<3>(), cst);
+      if (n < 4) {
+        read_one(R_, 2 * n, rst);
+        read_one(R_, 2 * n + 1, rst);
+      } else {
+        copy_rows(CR_, ic<(n & 3)>(), cst);
+      }
+      if (decltype(PART_)::value >= 0) emit_slot(ic<1 - H>(), ic<(decltype(PART_)::value & 1)>(), N_, d);
       __builtin_amdgcn_sched_barrier(0);
-    }
-    // this phase's reads are in registers, the copies that the next phase
-    // reads have landed (six phases of four come after them)
-    wait_copies<24>();
+    };
+    slot(ic<0>());
+    slot(ic<1>());
+    slot(ic<2>());
+    slot(ic<3>());
+    slot(ic<4>());
+    slot(ic<5>());
+    slot(ic<6>());
+    slot(ic<7>());
+    wait_copies<decltype(W_)::value>();
     __builtin_amdgcn_sched_barrier(0);
     barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
+  // Ends of phases: the phase's reads are in registers; the copies that the
+  // next phase reads have landed, after which six phases of four copies were
+  // issued, and in the epilogue's four phases S0, S1, S0, S1 stores.
+  constexpr int S1 = SWIGLU ? 6 : 10, S0 = 2 * NE - S1;
   uint32_t st = 0;  // stage of the K block being multiplied
-  auto block = [&](auto FIRST_, auto LAST_, auto LIVE_) __attribute__((always_inline)) {
-    constexpr bool LAST = decltype(LAST_)::value;
-    if (decltype(FIRST_)::value) scale_copy();
+  Done done{t, 0};  // the tile before, whose A1 is still to be stored
+  done.t.rows = 0;
+  auto block = [&](auto FIRST_, auto LAST_) __attribute__((always_inline)) {
+    constexpr bool FIRST = decltype(FIRST_)::value, LAST = decltype(LAST_)::value;
+    if (FIRST) scale_copy();
     if (LAST && tail) clear_tail(ic<0>());
-    phase(ic<0>(), ic<0>(), ic<3>(), st, ic<2>(), st, FIRST_, ic<1>());
-    phase(ic<0>(), ic<1>(), ic<1>(), st, ic<3>(), st, FIRST_, ic<1>());
-    if (LAST && tail) clear_tail(ic<1>());
-    if (LAST) emit_half(ic<0>());
-    phase(ic<1>(), ic<0>(), ic<0>(), st ^ 1, ic<1>(), st, FIRST_, LIVE_);
+    phase(ic<0>(), ic<0>(), ic<3>(), st, ic<2>(), st, FIRST_, ic<(FIRST ? 0 : -1)>(),
+          ic<24 + (FIRST ? 2 * S0 + S1 : 0)>(), done);
+    phase(ic<0>(), ic<1>(), ic<1>(), st, ic<3>(), st, FIRST_, ic<(FIRST ? 1 : -1)>(),
+          ic<24 + (FIRST ? 2 * S0 + 2 * S1 : 0)>(), done);
+    if (LAST) {
+      if (tail) clear_tail(ic<1>());
+      done = Done{t, to & 1};
+    }
+    phase(ic<1>(), ic<0>(), ic<0>(), st ^ 1, ic<1>(), st, FIRST_, ic<(LAST ? 0 : -1)>(),
+          ic<24 + (FIRST ? 2 * S0 + 2 * S1 : LAST ? S0 : 0)>(), done);
     copy_next();
-    phase(ic<1>(), ic<1>(), ic<2>(), st ^ 1, ic<0>(), st ^ 1, FIRST_, LIVE_);
-    if (LAST && decltype(LIVE_)::value) emit_half(ic<1>());
+    phase(ic<1>(), ic<1>(), ic<2>(), st ^ 1, ic<0>(), st ^ 1, FIRST_, ic<(LAST ? 1 : -1)>(),
+          ic<24 + (FIRST ? 2 * S0 + 2 * S1 : LAST ? S0 + S1 : 0)>(), done);
     st ^= 1;
   };
-  auto tile = [&](auto LIVE_) __attribute__((always_inline)) {
-    block(ic<1>(), ic<0>(), LIVE_);
-    for (int k = 1; k < nkb - 1; ++k) block(ic<0>(), ic<0>(), LIVE_);
-    block(ic<0>(), ic<1>(), LIVE_);
-  };
   for (; to < my_n; t = tile_at(t_g, ++to)) {
-    if (t.rows > 128) tile(ic<1>());
-    else tile(ic<0>());
+    block(ic<1>(), ic<0>());
+    for (int k = 1; k < nkb - 1; ++k) block(ic<0>(), ic<0>());
+    block(ic<0>(), ic<1>());
   }
+  auto flush = [&](auto N_) __attribute__((always_inline)) {
+    emit_slot(ic<1>(), ic<(decltype(N_)::value >> 3)>(), ic<(decltype(N_)::value & 7)>(), done);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  flush(ic<0>()); flush(ic<1>()); flush(ic<2>()); flush(ic<3>());
+  flush(ic<4>()); flush(ic<5>()); flush(ic<6>()); flush(ic<7>());
+  flush(ic<8>()); flush(ic<9>()); flush(ic<10>()); flush(ic<11>());
+  flush(ic<12>()); flush(ic<13>()); flush(ic<14>()); flush(ic<15>());
   wait_copies<0>();  // what was copied past the last tile lands before the LDS is released
 }
 
