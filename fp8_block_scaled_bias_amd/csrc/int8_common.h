@@ -31,5 +31,11 @@ __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f +
 // A_rows * K < 2^32.
 void launch_wide(const Args& a, bool swiglu, hipStream_t st);
 
+// 128 x 128 tiles (int8_mid.hip).  Requires, with an index, A_rows * K < 2^32.
+void launch_mid(const Args& a, bool swiglu, hipStream_t st);
+
+// The weights straight into registers (int8_stream.hip): any size.
+void launch_stream(const Args& a, bool swiglu, hipStream_t st);
+
 }  // namespace int8
 }  // namespace moe
