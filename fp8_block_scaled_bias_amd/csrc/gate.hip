@@ -10,9 +10,18 @@
 //   ds[e_j] += scale * (dw_j - sum_i dw_i s_i / S) / S   (renormalised)
 //   dl = s (ds - sum_e ds_e s_e)  (softmax),  ds s (1 - s)  (sigmoid)
 //
-// The order of the experts is that of the exact values: v is formed in 64
-// bits from the fp32 logits, so that two experts whose fp32 scores round to
-// the same number, or the wrong way round, are still told apart.
+// The order of the experts is that of the exact values: where the fp32 values
+// at the border between chosen and not chosen (of experts or of groups) are
+// nearer to each other than their error, a token is done again with v in 64
+// bits from the fp32 logits.  Without a bias the logits themselves are
+// ordered, and only equal ones need the second look.
+//
+// The floor is one read of the logits (16.8 MB of fp32 at 16384 x 256: 2.8 us);
+// the selection is what costs, so it is spread over four tokens a wave: 16
+// lanes hold a token (all 64 above 256 experts), a lane 4 C of its logits
+// (chunk c: experts 4 (16 c + lane) .. +3).  Each lane sorts its 8 largest,
+// then lists of 8 are merged across the lanes (DPP moves); the k-th entry is
+// the threshold that every lane compares its values with.
 #include "common.h"
 
 namespace moe {
@@ -43,23 +52,62 @@ __device__ __forceinline__ float load_logit<float>(const float* p) { return *p; 
 template <>
 __device__ __forceinline__ float load_logit<uint16_t>(const uint16_t* p) { return bf16_to_f32(*p); }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-  return v;
+__device__ __forceinline__ void load4(const float* p, float* v) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
 }
-template <typename F>
-__device__ __forceinline__ F wave_sum(F v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-  return v;
+__device__ __forceinline__ void load4(const uint16_t* p, float* v) {
+  const uint2 a = *reinterpret_cast<const uint2*>(p);
+  v[0] = bf16_to_f32(a.x & 0xFFFFu); v[1] = bf16_to_f32(a.x >> 16);
+  v[2] = bf16_to_f32(a.y & 0xFFFFu); v[3] = bf16_to_f32(a.y >> 16);
 }
 
-// One token by one wave; expert i * 64 + lane sits in slot i of a lane.
-// s_v: the wave's [E] doubles, s_g: its [GMAXG] doubles.
+// The value of a lane's partner in the merge rounds 0, 1, 2, 3 (of 16 lanes:
+// quad_perm [1,0,3,2] and [2,3,0,1], then the mirror lane of a half row and of
+// a row) and 4, 5 (xor 16 and 32): after round r a lane has combined 2^(r+1)
+// lanes, each once.
+template <int R>
+__device__ __forceinline__ int partner(int x) {
+  if (R == 0) return __builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, true);
+  if (R == 1) return __builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, true);
+  if (R == 2) return __builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, true);
+  if (R == 3) return __builtin_amdgcn_mov_dpp(x, 0x140, 0xF, 0xF, true);
+  return __shfl_xor(x, R == 4 ? 16 : 32, 64);
+}
+template <int R>
+__device__ __forceinline__ float partner(float v) { return __int_as_float(partner<R>(__float_as_int(v))); }
+template <int R>
+__device__ __forceinline__ double partner(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)partner<R>((int)(uint32_t)b), hi = (uint32_t)partner<R>((int)(b >> 32));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+template <int LPT, typename F, typename V>
+__device__ __forceinline__ V over_row(F f, V v) {
+  v = f(v, partner<0>(v));
+  v = f(v, partner<1>(v));
+  v = f(v, partner<2>(v));
+  v = f(v, partner<3>(v));
+  if (LPT == 64) {
+    v = f(v, partner<4>(v));
+    v = f(v, partner<5>(v));
+  }
+  return v;
+}
+template <int LPT, typename V>
+__device__ __forceinline__ V row_max(V v) { return over_row<LPT>([](V a, V b) { return max(a, b); }, v); }
+template <int LPT, typename V>
+__device__ __forceinline__ V row_sum(V v) { return over_row<LPT>([](V a, V b) { return a + b; }, v); }
+template <typename V>
+__device__ __forceinline__ V wave_sum(V v) { return row_sum<64>(v); }
+__device__ __forceinline__ float wave_max(float v) {
+  return over_row<64>([](float a, float b) { return fmaxf(a, b); }, v);
+}
+
+// One token by one wave, its order in 64 bits; expert i * 64 + lane sits in
+// slot i of a lane.  s_v: the wave's [E] doubles, s_g: its [GMAXG] doubles.
 template <typename D, int VPL>
-__device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double* s_v, double* s_g,
-                                           int* hist) {
+__device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double* s_v, double* s_g) {
   const int lane = threadIdx.x & 63;
   const D* row = static_cast<const D*>(a.logits) + t * a.E;
   const int E = a.E, size = E / a.n_group;
@@ -99,11 +147,6 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double*
       s[i] = 1.0f / (1.0f + expf(-l[i]));
     }
   }
-  if (a.scores) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (i * 64 + lane < E) a.scores[t * E + i * 64 + lane] = s[i];
-  }
   // values of the order; excluded experts (-inf or NaN) below every other,
   // slots that are no candidates at -inf
   const double kExcluded = -1.7e308;
@@ -124,8 +167,11 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double*
     __builtin_amdgcn_wave_barrier();
     if (lane < a.n_group) {
       double t1 = -INFINITY, t2 = -INFINITY;
+      int at = lane < size ? lane : 0;  // each lane begins at a place of its own: other banks
+#pragma unroll 4
       for (int i = 0; i < size; ++i) {
-        const double x = s_v[lane * size + i];
+        const double x = s_v[lane * size + at];
+        at = at + 1 == size ? 0 : at + 1;
         if (x > kExcluded) {
           t2 = fmax(t2, fmin(t1, x));
           t1 = fmax(t1, x);
@@ -156,15 +202,18 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double*
         best = v[i];
         at = i * 64 + lane;
       }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const double b = __shfl_xor(best, o, 64);
-      const int w = __shfl_xor(at, o, 64);
+    auto meet = [&](double b, int w) {
       if (b > best || (b == best && w < at)) {
         best = b;
         at = w;
       }
-    }
+    };
+    meet(partner<0>(best), partner<0>(at));
+    meet(partner<1>(best), partner<1>(at));
+    meet(partner<2>(best), partner<2>(at));
+    meet(partner<3>(best), partner<3>(at));
+    meet(partner<4>(best), partner<4>(at));
+    meet(partner<5>(best), partner<5>(at));
     if ((at & 63) == lane) taken |= 1u << (at >> 6);
   }
   // ids ascending: slots in order, lanes in order within a slot
@@ -183,26 +232,371 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double*
       a.topk_idx[o] = i * 64 + lane;
       const float w = a.renorm ? (sum > 0.f ? s[i] / sum : 0.f) : s[i];
       a.topk_w[o] = w * a.scale;
-      atomicAdd(&hist[i * 64 + lane], 1);
     }
     base += __popcll(msk);
   }
 }
 
-template <typename D, int VPL>
+// whole numbers in the order of the floats (and back): their maxima need no
+// care for NaN, which would cost an instruction each
+__device__ __forceinline__ int order_key(float x) {
+  const int b = __float_as_int(x);
+  return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float from_key(int b) { return __int_as_float(b ^ ((b >> 31) & 0x7FFFFFFF)); }
+
+__device__ __forceinline__ void order2(int& hi, int& lo) {
+  const int a = max(hi, lo), b = min(hi, lo);
+  hi = a;
+  lo = b;
+}
+// descending sort of 8 (19 exchanges), and of 8 that rise and then fall or
+// fall and then rise (12)
+__device__ __forceinline__ void sort8(int* v) {
+  order2(v[0], v[1]); order2(v[2], v[3]); order2(v[4], v[5]); order2(v[6], v[7]);
+  order2(v[0], v[2]); order2(v[1], v[3]); order2(v[4], v[6]); order2(v[5], v[7]);
+  order2(v[1], v[2]); order2(v[5], v[6]); order2(v[0], v[4]); order2(v[3], v[7]);
+  order2(v[1], v[5]); order2(v[2], v[6]);
+  order2(v[1], v[4]); order2(v[3], v[6]);
+  order2(v[2], v[4]); order2(v[3], v[5]);
+  order2(v[3], v[4]);
+}
+__device__ __forceinline__ void merge8(int* v) {
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & d)) order2(v[i], v[i + d]);
+}
+// a: the 8 largest of a and of b (both descending)
+__device__ __forceinline__ void join8(int* a, const int* b) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = max(a[i], b[7 - i]);
+  merge8(a);
+}
+template <int R>
+__device__ __forceinline__ void round8(int* a) {
+  int b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = partner<R>(a[i]);
+  join8(a, b);
+}
+
+// sum over the lanes up to this one (l: its place in the row)
+template <int LPT>
+__device__ __forceinline__ int row_scan(int v, int l) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);  // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+  if (LPT == 64) {
+    const int r0 = __builtin_amdgcn_readlane(v, 15), r1 = __builtin_amdgcn_readlane(v, 31),
+              r2 = __builtin_amdgcn_readlane(v, 47);
+    v += (l >= 16 ? r0 : 0) + (l >= 32 ? r1 : 0) + (l >= 48 ? r2 : 0);
+  }
+  return v;
+}
+
+// 1 / (1 + exp(-l)) with a relative error of 6 roundings at any l
+__device__ __forceinline__ float sigmoid_f32(float l) {
+  const float z = expf(-fabsf(l)), d = 1.0f + z;  // d in [1, 2]
+  float y = __builtin_amdgcn_rcpf(d);
+  y = fmaf(fmaf(-d, y, 1.0f), y, y);
+  return l >= 0.f ? y : z * y;
+}
+// exp(l - m), relative error (2.2 |l - m| + 2) roundings
+__device__ __forceinline__ float exp_from(float l, float m) {
+  return __builtin_amdgcn_exp2f((l - m) * 1.4426950408889634f);
+}
+
+// LPT lanes hold a token, each 4 C of its logits: expert 4 (LPT c + lane) + j
+// in slot 4 c + j.
+template <typename D, int LPT, int C>
 __global__ __launch_bounds__(GT) void gate_kernel(GateArgs a) {
-  __shared__ int hist[64 * VPL];
-  __shared__ double s_v[GT / 64][64 * VPL];
-  __shared__ double s_g[GT / 64][GMAXG];
-  for (int i = threadIdx.x; i < 64 * VPL; i += GT) hist[i] = 0;
+  constexpr int TPW = 64 / LPT, V = 4 * C, EMAX = LPT * V, W = GT / 64;
+  constexpr int PITCH = EMAX + 8;  // floats of a token's row in LDS: rows in different banks
+  constexpr int BYTES = TPW * PITCH * 4 > EMAX * 8 ? TPW * PITCH * 4 : EMAX * 8;
+  __shared__ __attribute__((aligned(16))) uint8_t s_mem[W][BYTES];
+  __shared__ __attribute__((aligned(16))) double s_g[W][GMAXG];
+  __shared__ __attribute__((aligned(16))) int s_ids[W][TPW][GMAXK];
+  if (blockIdx.x == 0)  // for the counting kernel
+    for (int e = threadIdx.x; e < a.E; e += GT) a.counts[e] = 0;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int sub = lane / LPT;
+  const int E = a.E, k = a.k;
+  const bool vec = (E & 3) == 0 && ((uintptr_t)a.logits & (4 * sizeof(D) - 1)) == 0;
+  const bool vec_out = (E & 3) == 0 && ((uintptr_t)a.scores & 15) == 0;
+  const int64_t step = (int64_t)gridDim.x * W * TPW, first = ((int64_t)blockIdx.x * W + wv) * TPW;
+  uint64_t any = 0;  // whether a token of this wave is left for the second look
+  for (int64_t t0 = first; t0 < a.T; t0 += step) {
+    const int64_t t = min(t0 + sub, a.T - 1);
+    const bool here = t0 + sub < a.T;
+    // (through an empty asm: what follows from the lane's place is formed in
+    // every round, not kept in registers for the next)
+    int l = lane & (LPT - 1);
+    asm volatile("" : "+v"(l));
+    const D* row = static_cast<const D*>(a.logits) + t * E;
+    float x[V], s[V];  // logits, then the values ordered; scores
+    if (vec && E == EMAX) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) load4(row + 4 * (LPT * c + l), x + 4 * c);
+    } else if (vec) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int e = 4 * (LPT * c + l);
+        load4(row + min(e, E - 4), x + 4 * c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[4 * c + j] = e < E ? x[4 * c + j] : -INFINITY;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = 4 * (LPT * (i >> 2) + l) + (i & 3);
+        const float y = load_logit(row + min(e, E - 1));
+        x[i] = e < E ? y : -INFINITY;
+      }
+    }
+    float m = 0.f, inv = 0.f, smax = 1.f;
+    if (a.softmax) {
+      int mk = order_key(x[0]);
+#pragma unroll
+      for (int i = 1; i < V; ++i) mk = max(mk, order_key(x[i]));
+      m = from_key(row_max<LPT>(mk));
+      m = m == -INFINITY ? 0.f : m;  // (no logit there: every score is 0)
+      float z = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        s[i] = exp_from(x[i], m);
+        z += s[i];
+      }
+      z = row_sum<LPT>(z);
+      smax = inv = z > 0.f ? 1.0f / z : 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] *= inv;
+    } else if (a.scores || a.bias || a.n_group > 1) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] = sigmoid_f32(x[i]);
+    }
+    if (a.scores && here) {
+      float* o = a.scores + t * E + 4 * l;
+      if (vec_out) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          if (4 * (LPT * c + l) < E)
+            *reinterpret_cast<float4*>(o + 4 * LPT * c) = make_float4(s[4 * c], s[4 * c + 1], s[4 * c + 2], s[4 * c + 3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (4 * (LPT * (i >> 2) + l) + (i & 3) < E) o[4 * LPT * (i >> 2) + (i & 3)] = s[i];
+      }
+    }
+    // fp32 scores are off by less than 2^-19 of the row's largest (softmax: 29
+    // roundings of 2^-24 - the exponent's 2.2 |x| e^x < 1, exp, 22 additions,
+    // the quotient) or 6 * 2^-24 (sigmoid); two that differ by more than 2^-17
+    // of it, or 2^-20, and the roundings of their sums with the bias are in
+    // their exact order
+    const float err = a.softmax ? 0x1p-17f * smax : 0x1p-20f;
+    bool redo = false;
+    // v, except that without a bias a choice of logits needs no rounding
+    const bool by_score = a.bias || a.group_top == 2;  // of the groups' values
+    if (a.bias) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = 4 * (LPT * (i >> 2) + l) + (i & 3);
+        x[i] = x[i] == -INFINITY ? -INFINITY : s[i] + a.bias[min(e, E - 1)];
+      }
+    }
+    if (a.n_group > 1) {
+      float* v = reinterpret_cast<float*>(s_mem[wv]) + sub * PITCH;
+      const bool of_scores = !a.bias && by_score;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          y[j] = of_scores && x[4 * c + j] != -INFINITY ? s[4 * c + j] : x[4 * c + j];
+        *reinterpret_cast<float4*>(v + 4 * (LPT * c + l)) = make_float4(y[0], y[1], y[2], y[3]);
+      }
+      __builtin_amdgcn_wave_barrier();
+      // lane g: the two largest of group g
+      const int size = E / a.n_group;
+      const float* mine_v = v + (l < a.n_group ? l : 0) * size;
+      float t1 = -INFINITY, t2 = -INFINITY;
+      auto take = [&](float y) {
+        t2 = __builtin_amdgcn_fmed3f(t1, t2, y);  // t2 <= t1: the second largest of the three
+        t1 = y > t1 ? y : t1;
+      };
+      if ((size & 3) == 0) {
+        const int n4 = size >> 2;
+        int at = l < n4 ? l : 0;  // each lane begins at a place of its own: other banks
+#pragma unroll 4
+        for (int i = 0; i < n4; ++i) {
+          const float4 y = *reinterpret_cast<const float4*>(mine_v + 4 * at);
+          take(y.x); take(y.y); take(y.z); take(y.w);
+          at = at + 1 == n4 ? 0 : at + 1;
+        }
+      } else {
+#pragma unroll 4
+        for (int i = 0; i < size; ++i) take(mine_v[i]);
+      }
+      const float worth = l >= a.n_group ? -INFINITY : a.group_top == 2 && t2 > -INFINITY ? t1 + t2 : t1;
+      constexpr int GL = LPT == 64 ? GMAXG : 16;
+      float* gs = reinterpret_cast<float*>(s_g[wv]) + 16 * sub;
+      if (l < GL) gs[l] = worth;
+      __builtin_amdgcn_wave_barrier();
+      const float near = by_score ? 2.f * err + 0x1p-21f * fabsf(worth) : 0.f;
+      int rank = 0, close = 0;
+#pragma unroll
+      for (int j = 0; j < GL; j += 4) {
+        const float4 y4 = *reinterpret_cast<const float4*>(gs + j);
+        const float y[4] = {y4.x, y4.y, y4.z, y4.w};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          rank += (y[h] > worth || (y[h] == worth && j + h < l)) ? 1 : 0;
+          close += y[h] >= worth - near ? 1 : 0;
+        }
+      }
+      const bool mine = l < a.n_group && rank < a.topk_group;
+      // (without scores equal groups are in their order already)
+      redo = by_score && mine && close > a.topk_group;
+      const uint32_t kept = (uint32_t)(__ballot(mine) >> (LPT == 64 ? 0 : 16 * sub));
+      const uint32_t magic = ((1u << 20) + size - 1) / size;  // e / size = e * magic >> 20 for e < 1024
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const uint32_t e = 4 * (LPT * c + l);
+        if ((size & 3) == 0) {
+          const bool in = (kept >> ((e * magic) >> 20)) & 1;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[4 * c + j] = in ? x[4 * c + j] : -INFINITY;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            x[4 * c + j] = (kept >> (((e + j) * magic) >> 20)) & 1 ? x[4 * c + j] : -INFINITY;
+        }
+      }
+    }
+    // the k-th largest
+    int top[8];
+    if (C == 1) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top[i] = i < 4 ? order_key(x[i]) : (int)0x80000000;
+      order2(top[0], top[1]); order2(top[2], top[3]); order2(top[0], top[2]);
+      order2(top[1], top[3]); order2(top[1], top[2]);
+    } else {
+#pragma unroll
+      for (int h = 0; h < V / 8; ++h) {
+        int w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = order_key(x[(8 * h + i) % V]);
+        sort8(w);
+        if (h == 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top[i] = w[i];
+        } else {
+          join8(top, w);
+        }
+      }
+    }
+    round8<0>(top);
+    round8<1>(top);
+    round8<2>(top);
+    round8<3>(top);
+    if (LPT == 64) {
+      round8<4>(top);
+      round8<5>(top);
+    }
+    int kth = top[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) kth = i < k ? top[i] : kth;
+    const float thr = from_key(kth);
+    const float least = a.bias ? thr - (err + 0x1p-21f * fabsf(thr)) : thr;
+    uint32_t mask = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) mask |= x[i] >= least ? 1u << i : 0u;
+    int over = row_sum<LPT>((int)__popc(mask)) - k;
+    if (!a.bias && __ballot(over > 0)) {
+      // equal logits at the border: of them, in the order of the experts
+      // (chunk, lane, place), the last `over` go
+      uint32_t equal = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) equal |= x[i] == thr ? 1u << i : 0u;
+      int room = row_sum<LPT>((int)__popc(equal)) - over;  // that stay
+      const bool ties = over > 0 && room > 0 && thr > -INFINITY;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const uint32_t of = (equal >> (4 * c)) & 15u;
+        const int n = __popc(of), upto = row_scan<LPT>(n, l);
+        int left = room - (upto - n);  // for this lane and those after it
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if ((of >> j) & 1) {
+            if (ties && left <= 0) mask &= ~(1u << (4 * c + j));
+            --left;
+          }
+        room -= row_sum<LPT>(n);
+      }
+      over = row_sum<LPT>((int)__popc(mask)) - k;
+    }
+    const int mine = __popc(mask);
+    redo = redo || over != 0;
+    const uint64_t again = __ballot(redo && here);
+    const bool clean = here && !((again >> (lane & ~(LPT - 1))) & (LPT == 64 ? ~0ull : 0xFFFFull));
+    any |= again;
+    // places of this lane's in the token's list: after those of the lanes before
+    const int upto = row_scan<LPT>(mine, l);
+    if (clean) {
+      int pos = upto - mine;
+      while (mask) {
+        const int i = __ffs(mask) - 1;
+        mask &= mask - 1;
+        s_ids[wv][sub][pos++] = 4 * (LPT * (i >> 2) + l) + (i & 3);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (clean && l < 16) {
+      float sj = 0.f;
+      int id = 0, place = 0;
+      if (l < k) {
+        id = s_ids[wv][sub][l];
+        for (int j = 0; j < k; ++j) place += s_ids[wv][sub][j] < id ? 1 : 0;
+        const float lj = load_logit(row + id);
+        sj = a.softmax ? exp_from(lj, m) * inv : sigmoid_f32(lj);
+      }
+      const float sum = row_sum<16>(sj);
+      if (l < k) {
+        a.topk_idx[t * k + place] = id;
+        a.topk_w[t * k + place] = a.scale * (a.renorm ? (sum > 0.f ? sj / sum : 0.f) : sj);
+      }
+    } else if (here && l == 0) {
+      a.topk_idx[t * k] = -1;  // for the second look
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  if (any) {
+    for (int64_t t0 = first; t0 < a.T; t0 += step) {
+      const bool in = lane < TPW && t0 + lane < a.T;
+      uint64_t todo = __ballot(in && ((volatile int32_t*)a.topk_idx)[(in ? t0 + lane : 0) * k] == -1);
+      for (; todo; todo &= todo - 1)
+        gate_token<D, EMAX / 64>(a, t0 + __ffsll((unsigned long long)todo) - 1,
+                                 reinterpret_cast<double*>(s_mem[wv]), s_g[wv]);
+    }
+  }
+}
+
+// counts[e] = how often e is named in ids (counts are 0 before, unless one
+// workgroup does it all).  Few workgroups, so that few add to one number.
+__global__ __launch_bounds__(1024) void gate_count_kernel(const int32_t* __restrict__ ids, int64_t n,
+                                                          int E, int32_t* __restrict__ counts) {
+  __shared__ int hist[GMAXE];
+  for (int e = threadIdx.x; e < E; e += 1024) hist[e] = 0;
   __syncthreads();
-  const int wv = threadIdx.x >> 6;
-  for (int64_t t = (int64_t)blockIdx.x * (GT / 64) + wv; t < a.T; t += (int64_t)gridDim.x * (GT / 64))
-    gate_token<D, VPL>(a, t, s_v[wv], s_g[wv], hist);
+  for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 1024)
+    atomicAdd(&hist[ids[i]], 1);
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += GT) {
+  for (int e = threadIdx.x; e < E; e += 1024) {
     const int c = hist[e];
-    if (c) atomicAdd(&a.counts[e], c);
+    if (gridDim.x == 1) counts[e] = c;
+    else if (c) atomicAdd(&counts[e], c);
   }
 }
 
@@ -308,14 +702,22 @@ __global__ __launch_bounds__(GT) void gate_backward_kernel(GateBwdArgs a) {
   }
 }
 
+template <typename D, int LPT, int C>
+void launch_gate_as(const GateArgs& a, hipStream_t st) {
+  const int64_t blocks = std::min<int64_t>(ceil_div(a.T, GT / LPT), 4096);
+  gate_kernel<D, LPT, C><<<dim3((unsigned)blocks), dim3(GT), 0, st>>>(a);
+  const int64_t n = a.T * a.k;
+  gate_count_kernel<<<dim3((unsigned)std::min<int64_t>(ceil_div(n, 4096), 64)), dim3(1024), 0, st>>>(
+      a.topk_idx, n, a.E, a.counts);
+}
+
 template <typename D>
 void launch_gate(const GateArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)std::min<int64_t>(ceil_div(a.T, GT / 64), 2048)), block(GT);
-  if (a.E <= 64) gate_kernel<D, 1><<<grid, block, 0, st>>>(a);
-  else if (a.E <= 128) gate_kernel<D, 2><<<grid, block, 0, st>>>(a);
-  else if (a.E <= 256) gate_kernel<D, 4><<<grid, block, 0, st>>>(a);
-  else if (a.E <= 512) gate_kernel<D, 8><<<grid, block, 0, st>>>(a);
-  else gate_kernel<D, 16><<<grid, block, 0, st>>>(a);
+  if (a.E > 512) launch_gate_as<D, 64, 4>(a, st);
+  else if (a.E > 256 || a.n_group > 16) launch_gate_as<D, 64, 2>(a, st);
+  else if (a.E > 128) launch_gate_as<D, 16, 4>(a, st);
+  else if (a.E > 64) launch_gate_as<D, 16, 2>(a, st);
+  else launch_gate_as<D, 16, 1>(a, st);
 }
 
 template <typename D>
@@ -378,8 +780,9 @@ extern "C" int moe_gate(const void* logits, int32_t logits_type, int64_t T, int3
                     ((uintptr_t)topk_w & 3) == 0 && ((uintptr_t)scores & 3) == 0,
                 "moe_gate: tensors must be aligned to their elements");
   }
-  gate_zero_kernel<<<1, GT, 0, st>>>(expert_counts, E);
-  if (T > 0) {
+  if (T == 0) {
+    gate_zero_kernel<<<1, GT, 0, st>>>(expert_counts, E);
+  } else {
     const GateArgs a{logits, bias, T, E, n_group, topk_group, group_top, k,
                      score == MOE_SCORE_SOFTMAX, renormalize != 0, scale,
                      topk_idx, topk_w, expert_counts, scores};
