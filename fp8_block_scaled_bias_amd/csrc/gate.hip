@@ -622,83 +622,142 @@ template <>
 __device__ __forceinline__ void store_grad<float>(float* p, float v) { *p = v; }
 template <>
 __device__ __forceinline__ void store_grad<uint16_t>(uint16_t* p, float v) { *p = (uint16_t)f32_to_bf16_rne(v); }
+__device__ __forceinline__ void store4(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(uint16_t* p, const float* v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
+}
 
-// One wave per token, expert i * 64 + lane in slot i.
-template <typename D, int VPL>
+// Lanes and slots as in gate_kernel.  Bound by its reads and writes of [T, E];
+// lane j < k of a token has its j-th choice (score from the logit again),
+// whose gradient goes into the row of ds in LDS, each place written once: of
+// an id named twice the first lane adds both.
+template <typename D, int LPT, int C>
 __global__ __launch_bounds__(GT) void gate_backward_kernel(GateBwdArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * (GT / 64) + (threadIdx.x >> 6);
-  if (t >= a.T) return;
-  const int E = a.E;
+  constexpr int TPW = 64 / LPT, V = 4 * C, EMAX = LPT * V, W = GT / 64;
+  __shared__ __attribute__((aligned(16))) float s_row[W][TPW][EMAX + 8];
+  __shared__ int s_id[W][TPW][GMAXK];
+  __shared__ float s_val[W][TPW][GMAXK];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int l = lane & (LPT - 1), sub = lane / LPT;
+  const int E = a.E, k = a.k;
+  const int64_t t0 = ((int64_t)blockIdx.x * W + wv) * TPW;
+  if (t0 >= a.T) return;
+  const bool here = t0 + sub < a.T;
+  const int64_t t = here ? t0 + sub : a.T - 1;
   const D* row = static_cast<const D*>(a.logits) + t * E;
-  float s[VPL], g[VPL];
-  float m = -INFINITY;
+  D* out = static_cast<D*>(a.dl) + t * E;
+  const bool vec = (E & 3) == 0 && (((uintptr_t)a.logits | (uintptr_t)a.dl) & (4 * sizeof(D) - 1)) == 0 &&
+                   ((uintptr_t)a.ds & 15) == 0;
+  float s[V], g[V];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = i * 64 + lane;
-    s[i] = e < E ? load_logit(row + e) : -INFINITY;
-    g[i] = a.ds && e < E ? a.ds[t * E + e] : 0.f;
-    m = fmaxf(m, s[i]);
-  }
-  if (a.softmax) {
-    m = wave_max(m);
-    float z = 0.f;
+  for (int i = 0; i < V; ++i) g[i] = 0.f;
+  if (vec) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      s[i] = s[i] == -INFINITY ? 0.f : expf(s[i] - m);
-      z += s[i];
+    for (int c = 0; c < C; ++c) {
+      const int e = 4 * (LPT * c + l);
+      load4(row + min(e, E - 4), s + 4 * c);
+      if (a.ds) load4(a.ds + t * E + min(e, E - 4), g + 4 * c);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[4 * c + j] = e < E ? s[4 * c + j] : -INFINITY;
+        g[4 * c + j] = e < E ? g[4 * c + j] : 0.f;
+      }
     }
-    z = wave_sum(z);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) s[i] = z > 0.f ? s[i] / z : 0.f;
   } else {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) s[i] = 1.0f / (1.0f + expf(-s[i]));
-  }
-  int id[GMAXK];
-  float dw[GMAXK], sj[GMAXK];
-  float S = 0.f, dot = 0.f;
-#pragma unroll
-  for (int j = 0; j < GMAXK; ++j) {
-    id[j] = -1;
-    dw[j] = sj[j] = 0.f;
-    if (j < a.k) {
-      const int e = a.idx[t * a.k + j];
-      if ((uint32_t)e < (uint32_t)E) {
-        id[j] = e;
-        dw[j] = a.scale * a.dw[t * a.k + j];
+    for (int i = 0; i < V; ++i) {
+      const int e = 4 * (LPT * (i >> 2) + l) + (i & 3);
+      const float y = load_logit(row + min(e, E - 1));
+      s[i] = e < E ? y : -INFINITY;
+      if (a.ds) {
+        const float d = a.ds[t * E + min(e, E - 1)];
+        g[i] = e < E ? d : 0.f;
       }
-      float mine = 0.f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (id[j] == i * 64 + lane) mine = s[i];
-      sj[j] = wave_sum(mine);
-      S += sj[j];
     }
   }
-  if (a.renorm) {
-#pragma unroll
-    for (int j = 0; j < GMAXK; ++j) dot = fmaf(dw[j], S > 0.f ? sj[j] / S : 0.f, dot);
-#pragma unroll
-    for (int j = 0; j < GMAXK; ++j) dw[j] = S > 0.f ? (dw[j] - dot) / S : 0.f;
+  int id = -1;
+  float lj = 0.f, dwj = 0.f;
+  if (l < k) {
+    const int e = a.idx[t * k + l];
+    if ((uint32_t)e < (uint32_t)E) {
+      id = e;
+      lj = load_logit(row + e);
+      dwj = a.scale * a.dw[t * k + l];
+    }
   }
+  float m = 0.f, inv = 0.f;
+  if (a.softmax) {
+    int mk = order_key(s[0]);
 #pragma unroll
-  for (int j = 0; j < GMAXK; ++j)
+    for (int i = 1; i < V; ++i) mk = max(mk, order_key(s[i]));
+    m = from_key(row_max<LPT>(mk));
+    m = m == -INFINITY ? 0.f : m;
+    float z = 0.f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (id[j] == i * 64 + lane) g[i] += dw[j];
+    for (int i = 0; i < V; ++i) {
+      s[i] = exp_from(s[i], m);
+      z += s[i];
+    }
+    z = row_sum<LPT>(z);
+    inv = z > 0.f ? 1.0f / z : 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] *= inv;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] = sigmoid_f32(s[i]);
+  }
+  // the choices' gradients (lanes 0..15 of a token; k <= 8)
+  float val = dwj;
+  if (a.renorm) {
+    const float sj = id < 0 ? 0.f : a.softmax ? exp_from(lj, m) * inv : sigmoid_f32(lj);
+    const float S = row_sum<16>(sj);
+    const float r = S > 0.f ? 1.0f / S : 0.f;
+    const float mean = row_sum<16>(dwj * sj * r);
+    val = (dwj - mean) * r;
+  }
+  float* buf = s_row[wv][sub];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    *reinterpret_cast<float4*>(buf + 4 * (LPT * c + l)) = make_float4(g[4 * c], g[4 * c + 1], g[4 * c + 2], g[4 * c + 3]);
+  if (l < k) {
+    s_id[wv][sub][l] = id;
+    s_val[wv][sub][l] = val;
+  }
+  __builtin_amdgcn_wave_barrier();
+  if (id >= 0) {
+    float sum = 0.f;
+    bool first = true;
+    for (int j = 0; j < k; ++j)
+      if (s_id[wv][sub][j] == id) {
+        first = first && j >= l;
+        sum += s_val[wv][sub][j];
+      }
+    if (first) buf[id] += sum;
+  }
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int c = 0; c < C; ++c) load4(buf + 4 * (LPT * c + l), g + 4 * c);
   float p = 0.f;
   if (a.softmax) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) p = fmaf(g[i], s[i], p);
-    p = wave_sum(p);
+    for (int i = 0; i < V; ++i) p = fmaf(g[i], s[i], p);
+    p = row_sum<LPT>(p);
   }
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = i * 64 + lane;
-    if (e < E)
-      store_grad(static_cast<D*>(a.dl) + t * E + e,
-                 a.softmax ? s[i] * (g[i] - p) : g[i] * s[i] * (1.0f - s[i]));
+  for (int i = 0; i < V; ++i) g[i] = a.softmax ? s[i] * (g[i] - p) : g[i] * s[i] * (1.0f - s[i]);
+  if (!here) return;
+  if (vec) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (4 * (LPT * c + l) < E) store4(out + 4 * (LPT * c + l), g + 4 * c);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = 4 * (LPT * (i >> 2) + l) + (i & 3);
+      if (e < E) store_grad(out + e, g[i]);
+    }
   }
 }
 
@@ -720,14 +779,18 @@ void launch_gate(const GateArgs& a, hipStream_t st) {
   else launch_gate_as<D, 16, 1>(a, st);
 }
 
+template <typename D, int LPT, int C>
+void launch_backward_as(const GateBwdArgs& a, hipStream_t st) {
+  gate_backward_kernel<D, LPT, C><<<dim3((unsigned)ceil_div(a.T, GT / LPT)), dim3(GT), 0, st>>>(a);
+}
+
 template <typename D>
 void launch_gate_backward(const GateBwdArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)ceil_div(a.T, GT / 64)), block(GT);
-  if (a.E <= 64) gate_backward_kernel<D, 1><<<grid, block, 0, st>>>(a);
-  else if (a.E <= 128) gate_backward_kernel<D, 2><<<grid, block, 0, st>>>(a);
-  else if (a.E <= 256) gate_backward_kernel<D, 4><<<grid, block, 0, st>>>(a);
-  else if (a.E <= 512) gate_backward_kernel<D, 8><<<grid, block, 0, st>>>(a);
-  else gate_backward_kernel<D, 16><<<grid, block, 0, st>>>(a);
+  if (a.E > 512) launch_backward_as<D, 64, 4>(a, st);
+  else if (a.E > 256) launch_backward_as<D, 64, 2>(a, st);
+  else if (a.E > 128) launch_backward_as<D, 16, 4>(a, st);
+  else if (a.E > 64) launch_backward_as<D, 16, 2>(a, st);
+  else launch_backward_as<D, 16, 1>(a, st);
 }
 
 int gate_shape(const char* who, int64_t T, int32_t E, int32_t type, int32_t score, int32_t k,
