@@ -105,47 +105,41 @@ __device__ __forceinline__ float wave_max(float v) {
 }
 
 // One token by one wave, its order in 64 bits; expert i * 64 + lane sits in
-// slot i of a lane.  s_v: the wave's [E] doubles, s_g: its [GMAXG] doubles.
+// slot i of a lane.  s_v: the wave's [64 VPL] doubles, s_g: its [GMAXG].  The
+// code is small (one exp in a rolled loop): it is read cold.
 template <typename D, int VPL>
 __device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double* s_v, double* s_g) {
   const int lane = threadIdx.x & 63;
   const D* row = static_cast<const D*>(a.logits) + t * a.E;
   const int E = a.E, size = E / a.n_group;
-  float l[VPL], s[VPL];
+  float l[VPL], s[VPL], bias[VPL];
   double v[VPL];
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = i * 64 + lane;
     l[i] = e < E ? load_logit(row + e) : -INFINITY;
+    bias[i] = a.bias && e < E ? a.bias[e] : 0.f;
     m = fmaxf(m, l[i]);
   }
-  m = wave_max(m);
-  if (a.softmax) {
-    double z = 0.0;
-    float zf = 0.f;
+  m = a.softmax ? wave_max(m) : 0.f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      // a row of -inf has no score at all
-      const bool there = l[i] != -INFINITY;
-      v[i] = there ? exp((double)l[i] - (double)m) : 0.0;
-      s[i] = there ? expf(l[i] - m) : 0.f;
-      z += v[i];
-      zf += s[i];
-    }
-    z = wave_sum(z);
-    zf = wave_sum(zf);
+  for (int i = 0; i < VPL; ++i) s_v[i * 64 + lane] = a.softmax ? (double)l[i] - (double)m : -fabs((double)l[i]);
+  double z = 0.0;
+#pragma unroll 1
+  for (int i = 0; i < VPL; ++i) {
+    const double x = s_v[i * 64 + lane];
+    const double y = x > -INFINITY ? exp(x) : 0.0;  // (a row of -inf has no score at all)
+    s_v[i * 64 + lane] = y;
+    z += y;
+  }
+  z = a.softmax ? wave_sum(z) : 0.0;
+  const double inv = z > 0.0 ? 1.0 / z : 0.0;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      v[i] = z > 0.0 ? v[i] / z : 0.0;
-      s[i] = zf > 0.f ? s[i] / zf : 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      v[i] = 1.0 / (1.0 + exp(-(double)l[i]));
-      s[i] = 1.0f / (1.0f + expf(-l[i]));
-    }
+  for (int i = 0; i < VPL; ++i) {
+    const double y = s_v[i * 64 + lane];
+    v[i] = a.softmax ? y * inv : (l[i] >= 0.f ? 1.0 : y) / (1.0 + y);
+    s[i] = (float)v[i];
   }
   // values of the order; excluded experts (-inf or NaN) below every other,
   // slots that are no candidates at -inf
@@ -158,7 +152,7 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double*
       v[i] = -INFINITY;
       continue;
     }
-    if (a.bias) v[i] += (double)a.bias[e];
+    v[i] += (double)bias[i];
     const double x = (a.bias || a.group_top == 2) ? v[i] : (double)l[i];
     if (a.n_group > 1) s_v[e] = order(x, l[i]);
     v[i] = order(a.bias ? v[i] : (double)l[i], l[i]);
