@@ -11,6 +11,8 @@ from ._lib import (SCORE_SIGMOID, SCORE_SOFTMAX, MoEError, fp8_quant_1x128, fp8_
                    moe_permute_workspace_bytes, moe_route,
                    moe_route_scores, moe_route_workspace_bytes, moe_router_backward,
                    moe_router_backward_dense, moe_router_backward_dense_workspace_bytes,
-                   moe_router_dcentroids, moe_router_logits, moe_router_logits_backward, moe_seq_balance, moe_seq_balance_workspace_bytes,
+                   moe_router_dcentroids, moe_router_logits, moe_router_logits_backward,
+                   moe_seq_balance, moe_seq_balance_workspace_bytes,
                    swiglu_backward, swiglu_backward_grouped, wgrad_chunks)
-from .layer import BackwardBuffers, Buffers, LayerShape, MoELayer  # noqa: F401
+from .layer import (BackwardBuffers, Buffers, Gate, Int8Buffers, Int8MoELayer, LayerShape,  # noqa: F401
+                    MoELayer)

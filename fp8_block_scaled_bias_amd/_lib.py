@@ -329,58 +329,89 @@ def moe_combine(expert_out_bf16, inv_perm, topk_w, shared_out_bf16, T, k, H, y_b
                  _dev(shared_out_bf16), T, k, H, _dev(y_bf16), _stream(stream))
 
 
+_f32t, _bf16t, _i32t, _i8t = torch.float32, torch.bfloat16, torch.int32, torch.int8
+
+
+def _ptr(t, dtype, dev):
+    """Device pointer of a contiguous tensor of the given type on the current
+    GPU `dev`, where the call's kernels run (None -> NULL).  dtype None: any."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"expected a torch.Tensor, got {type(t)}")
+    if t.get_device() != dev or not t.is_contiguous() or (dtype is not None and t.dtype is not dtype):
+        if t.is_cuda and t.get_device() != dev:
+            raise ValueError(f"tensor is on GPU {t.get_device()}, the current one is {dev}")
+        _dev(t)
+        raise TypeError(f"expected a tensor of {dtype}, got {t.dtype}")
+    return t.data_ptr()
+
+
 def _logits_type(t):
-    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.float32, torch.bfloat16):
+    if not isinstance(t, torch.Tensor) or t.dtype not in (_f32t, _bf16t):
         raise TypeError("logits must be a float32 or bfloat16 torch.Tensor")
-    return TYPE_F32 if t.dtype == torch.float32 else TYPE_BF16
+    return TYPE_F32 if t.dtype == _f32t else TYPE_BF16
 
 
 def moe_router_logits(x_bf16, T, H, centroids, E, logits, workspace, workspace_bytes, stream=None):
-    return _call("moe_router_logits", _dev(x_bf16), T, H, _dev(centroids), E, _dev(logits),
-                 _dev(workspace), workspace_bytes, _stream(stream))
+    d = torch.cuda.current_device()
+    return _call("moe_router_logits", _ptr(x_bf16, _bf16t, d), T, H, _ptr(centroids, _f32t, d), E,
+                 _ptr(logits, _f32t, d), _ptr(workspace, None, d), workspace_bytes, _stream(stream))
 
 
 def moe_router_logits_backward(x_bf16, centroids, d_logits, T, H, E, dx_in_bf16, dx_out_bf16,
                                d_centroids, workspace, workspace_bytes, stream=None):
-    return _call("moe_router_logits_backward", _dev(x_bf16), _dev(centroids), _dev(d_logits), T, H, E,
-                 _dev(dx_in_bf16), _dev(dx_out_bf16), _dev(d_centroids), _dev(workspace),
+    d = torch.cuda.current_device()
+    return _call("moe_router_logits_backward", _ptr(x_bf16, _bf16t, d), _ptr(centroids, _f32t, d),
+                 _ptr(d_logits, _f32t, d), T, H, E, _ptr(dx_in_bf16, _bf16t, d),
+                 _ptr(dx_out_bf16, _bf16t, d), _ptr(d_centroids, _f32t, d), _ptr(workspace, None, d),
                  workspace_bytes, _stream(stream))
 
 
 def moe_gate(logits, T, E, bias, score, n_group, topk_group, group_top, k, renormalize, scale,
              topk_idx, topk_w, expert_counts, stream=None, *, scores=None):
-    return _call("moe_gate", _dev(logits), _logits_type(logits), T, E, _dev(bias), score, n_group,
-                 topk_group, group_top, k, int(renormalize), scale, _dev(topk_idx), _dev(topk_w),
-                 _dev(expert_counts), _dev(scores), _stream(stream))
+    d = torch.cuda.current_device()
+    kind = _logits_type(logits)
+    return _call("moe_gate", _ptr(logits, None, d), kind, T, E, _ptr(bias, _f32t, d), score, n_group,
+                 topk_group, group_top, k, int(renormalize), scale, _ptr(topk_idx, _i32t, d),
+                 _ptr(topk_w, _f32t, d), _ptr(expert_counts, _i32t, d), _ptr(scores, _f32t, d),
+                 _stream(stream))
 
 
 def moe_gate_backward(logits, T, E, score, k, renormalize, scale, topk_idx, d_topk_w, d_logits,
                       stream=None, *, d_scores=None):
-    if isinstance(d_logits, torch.Tensor) and d_logits.dtype != logits.dtype:
-        raise TypeError("d_logits must have the logits' type")
-    return _call("moe_gate_backward", _dev(logits), _logits_type(logits), T, E, score, k,
-                 int(renormalize), scale, _dev(topk_idx), _dev(d_topk_w), _dev(d_scores),
-                 _dev(d_logits), _stream(stream))
+    d = torch.cuda.current_device()
+    kind = _logits_type(logits)
+    return _call("moe_gate_backward", _ptr(logits, None, d), kind, T, E, score, k, int(renormalize),
+                 scale, _ptr(topk_idx, _i32t, d), _ptr(d_topk_w, _f32t, d), _ptr(d_scores, _f32t, d),
+                 _ptr(d_logits, logits.dtype, d), _stream(stream))
 
 
 def int8_quant_rows(in_bf16, M, K, ld_in, out_int8, scales, stream=None):
-    return _call("int8_quant_rows", _dev(in_bf16), M, K, ld_in, _dev(out_int8), _dev(scales),
-                 _stream(stream))
+    d = torch.cuda.current_device()
+    return _call("int8_quant_rows", _ptr(in_bf16, _bf16t, d), M, K, ld_in, _ptr(out_int8, _i8t, d),
+                 _ptr(scales, _f32t, d), _stream(stream))
 
 
 def int8_quant_channels(w_f32, G, N, K, out_int8, scales, stream=None):
-    return _call("int8_quant_channels", _dev(w_f32), G, N, K, _dev(out_int8), _dev(scales),
-                 _stream(stream))
+    d = torch.cuda.current_device()
+    return _call("int8_quant_channels", _ptr(w_f32, _f32t, d), G, N, K, _ptr(out_int8, _i8t, d),
+                 _ptr(scales, _f32t, d), _stream(stream))
 
 
 def grouped_int8_gemm(A, A_scale, a_row_index, B, B_scale, group_offsets, G, M_total, N, K, C_bf16,
                       stream=None):
-    return _call("grouped_int8_gemm", _dev(A), _dev(A_scale), _dev(a_row_index), _rows(A), _dev(B),
-                 _dev(B_scale), _dev(group_offsets), G, M_total, N, K, _dev(C_bf16), _stream(stream))
+    d = torch.cuda.current_device()
+    return _call("grouped_int8_gemm", _ptr(A, _i8t, d), _ptr(A_scale, _f32t, d),
+                 _ptr(a_row_index, _i32t, d), _rows(A), _ptr(B, _i8t, d), _ptr(B_scale, _f32t, d),
+                 _ptr(group_offsets, _i32t, d), G, M_total, N, K, _ptr(C_bf16, _bf16t, d),
+                 _stream(stream))
 
 
 def grouped_int8_gemm_swiglu(A, A_scale, a_row_index, B, B_scale, group_offsets, G, M_total, I, K,
                              H_bf16, stream=None):
-    return _call("grouped_int8_gemm_swiglu", _dev(A), _dev(A_scale), _dev(a_row_index), _rows(A),
-                 _dev(B), _dev(B_scale), _dev(group_offsets), G, M_total, I, K, _dev(H_bf16),
+    d = torch.cuda.current_device()
+    return _call("grouped_int8_gemm_swiglu", _ptr(A, _i8t, d), _ptr(A_scale, _f32t, d),
+                 _ptr(a_row_index, _i32t, d), _rows(A), _ptr(B, _i8t, d), _ptr(B_scale, _f32t, d),
+                 _ptr(group_offsets, _i32t, d), G, M_total, I, K, _ptr(H_bf16, _bf16t, d),
                  _stream(stream))

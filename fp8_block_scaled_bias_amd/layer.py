@@ -44,6 +44,21 @@ reads inside the GEMM), so the backward keeps nothing derived from the
 weights: after a weight update (requantize_from_fp32, or any write to w_gu /
 w_dn) the next forward and backward use the new weights as they are.
 
+With a Gate, the router is moe_router_logits + moe_gate instead of moe_route
+(softmax scores, weights that are not renormalised, a scale, no bias, other
+groups), and its backward moe_gate_backward + moe_router_logits_backward.
+
+Int8MoELayer is the layer's forward with the experts in 8-bit integers (a scale
+for each token and each output channel):
+
+  1. the router, as above
+  2. int8_quant_rows        x (on the side stream)
+  3. moe_permute
+  4. grouped_int8_gemm_swiglu   h = silu(gate) up, bf16
+  5. int8_quant_rows        h
+  6. grouped_int8_gemm      down projection
+  7. moe_combine
+
 torch is only used to hold device memory and to name the stream; every step
 runs in the library's HIP kernels.
 """
@@ -71,6 +86,19 @@ class LayerShape:
         return self.E + self.n_shared
 
 
+@dataclasses.dataclass(frozen=True)
+class Gate:
+    """A router in one of moe_gate's forms: score SCORE_SOFTMAX or
+    SCORE_SIGMOID; use_bias: the layer's bias moves the choice; groups (of the
+    shape) by their group_top largest; renormalize: a token's weights sum to
+    scale, else they are scale times the scores."""
+    score: int = L.SCORE_SOFTMAX
+    use_bias: bool = True
+    group_top: int = 2
+    renormalize: bool = True
+    scale: float = 1.0
+
+
 class Buffers:
     """Device buffers of one forward at T tokens (reused across calls)."""
 
@@ -94,6 +122,7 @@ class Buffers:
         self.perm_ws_bytes = max(16, L.moe_permute_workspace_bytes(T, s.k, s.E))
         self.perm_ws = torch.empty((self.perm_ws_bytes,), dtype=u8, device=dev)
         self._hgu = None
+        self._logits = None
         self._dev = dev
         self._shape = s
         self.hq = torch.empty((R, s.I), dtype=u8, device=dev)
@@ -118,6 +147,15 @@ class Buffers:
             self.seq_ws = torch.empty((self.seq_ws_bytes,), dtype=torch.uint8, device=dev)
             self._seq_len = seq_len
         return self
+
+    @property
+    def logits(self):
+        """fp32 router logits [T, E] of a layer with a Gate, which its backward
+        reads (allocated on first use)."""
+        if self._logits is None:
+            self._logits = torch.empty((self.T, self._shape.E), dtype=torch.float32,
+                                       device=self._dev)
+        return self._logits
 
     @property
     def hgu(self):
@@ -197,8 +235,10 @@ class MoELayer:
     Group E (the last) is the shared expert.
     """
 
-    def __init__(self, shape: LayerShape, centroids, bias, w_gu, w_gu_s, w_dn, w_dn_s):
+    def __init__(self, shape: LayerShape, centroids, bias, w_gu, w_gu_s, w_dn, w_dn_s,
+                 gate: Gate | None = None):
         self.shape = shape
+        self.gate = gate
         self.centroids = centroids
         self.bias = bias
         self.w_gu, self.w_gu_s, self.w_dn, self.w_dn_s = w_gu, w_gu_s, w_dn, w_dn_s
@@ -223,12 +263,12 @@ class MoELayer:
 
     @classmethod
     def from_fp32_experts(cls, shape: LayerShape, centroids, bias, gu_fp32, dn_fp32,
-                          device="cuda"):
+                          device="cuda", gate: Gate | None = None):
         """Build a layer from per-expert fp32 weights, quantised on the GPU.
 
         gu_fp32 / dn_fp32: iterables of (expert, array [2I, H] / [H, I]) covering
         every group 0..G-1 (G-1 is the shared expert).  Each array is copied
-        to the GPU and quantised in 128x128 blocks by fp8_quant_128x128.
+        to the GPU and quantised there (quantize_into).
         """
         w_gu, w_gu_s, w_dn, w_dn_s = cls.empty_weights(shape, device)
         stream = torch.cuda.current_stream()
@@ -237,7 +277,7 @@ class MoELayer:
                 t = torch.from_numpy(arr).to(device)
                 cls.quantize_into(t[None], q[e:e + 1], s[e:e + 1], stream)
                 stream.synchronize()
-        return cls(shape, centroids, bias, w_gu, w_gu_s, w_dn, w_dn_s)
+        return cls(shape, centroids, bias, w_gu, w_gu_s, w_dn, w_dn_s, gate)
 
     def buffers(self, T: int) -> Buffers:
         b = self._bufs.get(T)
@@ -421,7 +461,18 @@ class MoELayer:
                                       cap, st),
             L.grouped_fp8_wgrad(bb.c_dgu, bb.s_dgu, bb.c_x, bb.s_x, cap, b.offsets, G, R, 2 * I, H,
                                 bb.dW_gu, st)))
-        if seq_len is None:
+        if self.gate is not None:
+            if seq_len is not None:
+                raise ValueError("the sequence-wise balance term needs moe_route's scores: no Gate")
+            g = self.gate
+            bb.dense()
+            step("router_bwd", lambda: (
+                L.moe_gate_backward(b.logits, T, s.E, g.score, k, g.renormalize, g.scale, b.topk_idx,
+                                    bb.dw, bb.dlogit[:T], st),
+                L.moe_router_logits_backward(x_bf16, self.centroids, bb.dlogit[:T], T, H, s.E, bb.dx,
+                                             bb.dx_total, bb.dC, bb.dense_ws, bb.dense_ws_bytes,
+                                             st)))
+        elif seq_len is None:
             step("router_bwd", lambda: (
                 L.moe_router_backward(x_bf16, self.centroids, b.topk_idx, bb.dw, b.inv_perm, bb.dx,
                                       T, H, s.E, k, bb.dx_total, bb.dlogit_rows, st,
@@ -441,7 +492,16 @@ class MoELayer:
     def _route(self, x_bf16, b, seq_len, stream):
         s = self.shape
         T = x_bf16.shape[0]
-        if seq_len is None:
+        if self.gate is not None:
+            if seq_len is not None:
+                raise ValueError("the sequence-wise balance term needs moe_route's scores: no Gate")
+            g = self.gate
+            L.moe_router_logits(x_bf16, T, s.H, self.centroids, s.E, b.logits, b.route_ws,
+                                b.route_ws_bytes, stream)
+            L.moe_gate(b.logits, T, s.E, self.bias if g.use_bias else None, g.score, s.n_group,
+                       s.topk_group, g.group_top, s.k, g.renormalize, g.scale, b.topk_idx, b.topk_w,
+                       b.counts, stream)
+        elif seq_len is None:
             L.moe_route(x_bf16, T, s.H, self.centroids, self.bias, s.E, s.n_group, s.topk_group,
                         s.k, b.topk_idx, b.topk_w, b.counts, b.route_ws, b.route_ws_bytes, stream,
                         topk_s=b.topk_s)
@@ -456,3 +516,83 @@ class MoELayer:
         L.moe_seq_balance(b.scores, b.score_sums, b.topk_idx, b.T, s.E, s.k, seq_len, alpha,
                           b.seq_f, b.seq_p, b.seq_loss, b.seq_ws, b.seq_ws_bytes, stream)
 
+
+class Int8Buffers(Buffers):
+    """Device buffers of one int8 forward at T tokens (reused across calls)."""
+
+    def __init__(self, shape: LayerShape, T: int, device="cuda"):
+        super().__init__(shape, T, device)
+        s, R, dev = shape, self.R, self._dev
+        i8, f32 = torch.int8, torch.float32
+        self.xq = torch.empty((T, s.H), dtype=i8, device=dev)
+        self.xs = torch.empty((T,), dtype=f32, device=dev)
+        self.h = torch.empty((R, s.I), dtype=torch.bfloat16, device=dev)
+        self.hq = torch.empty((R, s.I), dtype=i8, device=dev)
+        self.hs = torch.empty((R,), dtype=f32, device=dev)
+
+
+class Int8MoELayer(MoELayer):
+    """The layer's forward with expert weights and activations in 8-bit integers.
+
+      w_gu [G, 2I, H] int8 (rows [0, I) gate, [I, 2I) up), w_gu_s [G, 2I] fp32
+      w_dn [G, H, I],                                       w_dn_s [G, H]
+    Built by from_fp32_experts like MoELayer; inference only.
+    """
+
+    @staticmethod
+    def empty_weights(shape: LayerShape, device="cuda"):
+        s, dev = shape, torch.device(device)
+        return (torch.empty((s.G, 2 * s.I, s.H), dtype=torch.int8, device=dev),
+                torch.empty((s.G, 2 * s.I), dtype=torch.float32, device=dev),
+                torch.empty((s.G, s.H, s.I), dtype=torch.int8, device=dev),
+                torch.empty((s.G, s.H), dtype=torch.float32, device=dev))
+
+    @staticmethod
+    def quantize_into(w_f32, out_q, out_s, stream=None):
+        """Quantisation of fp32 weights [G', N, K], one scale an output channel."""
+        G, N, K = w_f32.shape
+        L.int8_quant_channels(w_f32, G, N, K, out_q, out_s, stream)
+
+    def buffers(self, T: int) -> Int8Buffers:
+        b = self._bufs.get(T)
+        if b is None:
+            b = self._bufs[T] = Int8Buffers(self.shape, T, self.centroids.device)
+        return b
+
+    def forward(self, x_bf16: torch.Tensor, bufs: Int8Buffers | None = None, stream=None,
+                update_bias: bool = False, gamma: float = 0.001) -> torch.Tensor:
+        """One layer forward (x's quantisation beside the router, as in
+        MoELayer.forward)."""
+        s = self.shape
+        T = x_bf16.shape[0]
+        b = bufs or self.buffers(T)
+        R = b.R
+        st = stream if stream is not None else torch.cuda.current_stream()
+        if self._side is None:
+            self._side = torch.cuda.Stream(device=st.device)
+        side = self._side
+        side.wait_stream(st)
+        L.int8_quant_rows(x_bf16, T, s.H, s.H, b.xq, b.xs, side)
+        self._route(x_bf16, b, None, st)
+        L.moe_permute(b.topk_idx, b.counts, T, s.k, s.E, s.n_shared, b.offsets, b.perm_src,
+                      b.inv_perm, None, None, s.H, None, None, b.perm_ws, b.perm_ws_bytes, st)
+        st.wait_stream(side)
+        L.grouped_int8_gemm_swiglu(b.xq, b.xs, b.perm_src, self.w_gu, self.w_gu_s, b.offsets, s.G,
+                                   R, s.I, s.H, b.h, st)
+        L.int8_quant_rows(b.h, R, s.I, s.I, b.hq, b.hs, st)
+        L.grouped_int8_gemm(b.hq, b.hs, None, self.w_dn, self.w_dn_s, b.offsets, s.G, R, s.H, s.I,
+                            b.d, st)
+        shared = b.d[T * s.k:T * s.k + T] if s.n_shared else None
+        L.moe_combine(b.d, b.inv_perm, b.topk_w, shared, T, s.k, s.H, b.y, st)
+        if update_bias:
+            L.moe_bias_update(b.counts, self.bias, s.E, gamma, st)
+        return b.y
+
+    def requantize_from_fp32(self, gu_fp32, dn_fp32, stream=None):
+        """Requantise both weight sets in place from fp32 weights ([G, 2I, H]
+        and [G, H, I] device tensors)."""
+        self.quantize_into(gu_fp32, self.w_gu, self.w_gu_s, stream)
+        self.quantize_into(dn_fp32, self.w_dn, self.w_dn_s, stream)
+
+    def backward(self, *args, **kw):
+        raise NotImplementedError("Int8MoELayer is a forward only: train with MoELayer")
