@@ -107,8 +107,9 @@ __device__ __forceinline__ float wave_max(float v) {
 // One token by one wave, its order in 64 bits; expert i * 64 + lane sits in
 // slot i of a lane.  s_v: the wave's [64 VPL] doubles, s_g: its [GMAXG].  The
 // code is small (one exp in a rolled loop): it is read cold.
-template <typename D, int VPL>
-__device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double* s_v, double* s_g) {
+template <typename D, int VPL, bool ONE>
+__device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double* s_v, double* s_g,
+                                           int* s_hist) {
   const int lane = threadIdx.x & 63;
   const D* row = static_cast<const D*>(a.logits) + t * a.E;
   const int E = a.E, size = E / a.n_group;
@@ -226,6 +227,7 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double*
       a.topk_idx[o] = i * 64 + lane;
       const float w = a.renorm ? (sum > 0.f ? s[i] / sum : 0.f) : s[i];
       a.topk_w[o] = w * a.scale;
+      if (ONE) atomicAdd(&s_hist[i * 64 + lane], 1);
     }
     base += __popcll(msk);
   }
@@ -304,8 +306,8 @@ __device__ __forceinline__ float exp_from(float l, float m) {
 }
 
 // LPT lanes hold a token, each 4 C of its logits: expert 4 (LPT c + lane) + j
-// in slot 4 c + j.
-template <typename D, int LPT, int C>
+// in slot 4 c + j.  ONE: a single workgroup, which counts the choices itself.
+template <typename D, int LPT, int C, bool ONE>
 __global__ __launch_bounds__(GT) void gate_kernel(GateArgs a) {
   constexpr int TPW = 64 / LPT, V = 4 * C, EMAX = LPT * V, W = GT / 64;
   constexpr int PITCH = EMAX + 8;  // floats of a token's row in LDS: rows in different banks
@@ -313,8 +315,13 @@ __global__ __launch_bounds__(GT) void gate_kernel(GateArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t s_mem[W][BYTES];
   __shared__ __attribute__((aligned(16))) double s_g[W][GMAXG];
   __shared__ __attribute__((aligned(16))) int s_ids[W][TPW][GMAXK];
-  if (blockIdx.x == 0)  // for the counting kernel
+  __shared__ int s_hist[ONE ? EMAX : 1];
+  if (ONE) {
+    for (int e = threadIdx.x; e < a.E; e += GT) s_hist[e] = 0;
+    __syncthreads();
+  } else if (blockIdx.x == 0) {  // for the counting kernel
     for (int e = threadIdx.x; e < a.E; e += GT) a.counts[e] = 0;
+  }
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int sub = lane / LPT;
   const int E = a.E, k = a.k;
@@ -560,6 +567,7 @@ __global__ __launch_bounds__(GT) void gate_kernel(GateArgs a) {
       if (l < k) {
         a.topk_idx[t * k + place] = id;
         a.topk_w[t * k + place] = a.scale * (a.renorm ? (sum > 0.f ? sj / sum : 0.f) : sj);
+        if (ONE) atomicAdd(&s_hist[id], 1);
       }
     } else if (here && l == 0) {
       a.topk_idx[t * k] = -1;  // for the second look
@@ -571,14 +579,19 @@ __global__ __launch_bounds__(GT) void gate_kernel(GateArgs a) {
       const bool in = lane < TPW && t0 + lane < a.T;
       uint64_t todo = __ballot(in && ((volatile int32_t*)a.topk_idx)[(in ? t0 + lane : 0) * k] == -1);
       for (; todo; todo &= todo - 1)
-        gate_token<D, EMAX / 64>(a, t0 + __ffsll((unsigned long long)todo) - 1,
-                                 reinterpret_cast<double*>(s_mem[wv]), s_g[wv]);
+        gate_token<D, EMAX / 64, ONE>(a, t0 + __ffsll((unsigned long long)todo) - 1,
+                                      reinterpret_cast<double*>(s_mem[wv]), s_g[wv], s_hist);
     }
+  }
+  if (ONE) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += GT) a.counts[e] = s_hist[e];
   }
 }
 
 // counts[e] = how often e is named in ids (counts are 0 before, unless one
-// workgroup does it all).  Few workgroups, so that few add to one number.
+// workgroup does it all).  A launch of its own costs 1 us less than adding up
+// in gate_kernel's loop, whose registers and adds take longer (16384 tokens).  Few workgroups, so that few add to one number.
 __global__ __launch_bounds__(1024) void gate_count_kernel(const int32_t* __restrict__ ids, int64_t n,
                                                           int E, int32_t* __restrict__ counts) {
   __shared__ int hist[GMAXE];
@@ -758,7 +771,11 @@ __global__ __launch_bounds__(GT) void gate_backward_kernel(GateBwdArgs a) {
 template <typename D, int LPT, int C>
 void launch_gate_as(const GateArgs& a, hipStream_t st) {
   const int64_t blocks = std::min<int64_t>(ceil_div(a.T, GT / LPT), 4096);
-  gate_kernel<D, LPT, C><<<dim3((unsigned)blocks), dim3(GT), 0, st>>>(a);
+  if (blocks == 1) {
+    gate_kernel<D, LPT, C, true><<<dim3(1), dim3(GT), 0, st>>>(a);
+    return;
+  }
+  gate_kernel<D, LPT, C, false><<<dim3((unsigned)blocks), dim3(GT), 0, st>>>(a);
   const int64_t n = a.T * a.k;
   gate_count_kernel<<<dim3((unsigned)std::min<int64_t>(ceil_div(n, 4096), 64)), dim3(1024), 0, st>>>(
       a.topk_idx, n, a.E, a.counts);
