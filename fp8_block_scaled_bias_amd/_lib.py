@@ -347,6 +347,11 @@ def _ptr(t, dtype, dev):
     return t.data_ptr()
 
 
+def _on(stream, dev):
+    """_stream, with the current stream's handle taken directly."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
 def _logits_type(t):
     if not isinstance(t, torch.Tensor) or t.dtype not in (_f32t, _bf16t):
         raise TypeError("logits must be a float32 or bfloat16 torch.Tensor")
@@ -356,7 +361,7 @@ def _logits_type(t):
 def moe_router_logits(x_bf16, T, H, centroids, E, logits, workspace, workspace_bytes, stream=None):
     d = torch.cuda.current_device()
     return _call("moe_router_logits", _ptr(x_bf16, _bf16t, d), T, H, _ptr(centroids, _f32t, d), E,
-                 _ptr(logits, _f32t, d), _ptr(workspace, None, d), workspace_bytes, _stream(stream))
+                 _ptr(logits, _f32t, d), _ptr(workspace, None, d), workspace_bytes, _on(stream, d))
 
 
 def moe_router_logits_backward(x_bf16, centroids, d_logits, T, H, E, dx_in_bf16, dx_out_bf16,
@@ -365,7 +370,7 @@ def moe_router_logits_backward(x_bf16, centroids, d_logits, T, H, E, dx_in_bf16,
     return _call("moe_router_logits_backward", _ptr(x_bf16, _bf16t, d), _ptr(centroids, _f32t, d),
                  _ptr(d_logits, _f32t, d), T, H, E, _ptr(dx_in_bf16, _bf16t, d),
                  _ptr(dx_out_bf16, _bf16t, d), _ptr(d_centroids, _f32t, d), _ptr(workspace, None, d),
-                 workspace_bytes, _stream(stream))
+                 workspace_bytes, _on(stream, d))
 
 
 def moe_gate(logits, T, E, bias, score, n_group, topk_group, group_top, k, renormalize, scale,
@@ -375,7 +380,7 @@ def moe_gate(logits, T, E, bias, score, n_group, topk_group, group_top, k, renor
     return _call("moe_gate", _ptr(logits, None, d), kind, T, E, _ptr(bias, _f32t, d), score, n_group,
                  topk_group, group_top, k, int(renormalize), scale, _ptr(topk_idx, _i32t, d),
                  _ptr(topk_w, _f32t, d), _ptr(expert_counts, _i32t, d), _ptr(scores, _f32t, d),
-                 _stream(stream))
+                 _on(stream, d))
 
 
 def moe_gate_backward(logits, T, E, score, k, renormalize, scale, topk_idx, d_topk_w, d_logits,
@@ -384,19 +389,19 @@ def moe_gate_backward(logits, T, E, score, k, renormalize, scale, topk_idx, d_to
     kind = _logits_type(logits)
     return _call("moe_gate_backward", _ptr(logits, None, d), kind, T, E, score, k, int(renormalize),
                  scale, _ptr(topk_idx, _i32t, d), _ptr(d_topk_w, _f32t, d), _ptr(d_scores, _f32t, d),
-                 _ptr(d_logits, logits.dtype, d), _stream(stream))
+                 _ptr(d_logits, logits.dtype, d), _on(stream, d))
 
 
 def int8_quant_rows(in_bf16, M, K, ld_in, out_int8, scales, stream=None):
     d = torch.cuda.current_device()
     return _call("int8_quant_rows", _ptr(in_bf16, _bf16t, d), M, K, ld_in, _ptr(out_int8, _i8t, d),
-                 _ptr(scales, _f32t, d), _stream(stream))
+                 _ptr(scales, _f32t, d), _on(stream, d))
 
 
 def int8_quant_channels(w_f32, G, N, K, out_int8, scales, stream=None):
     d = torch.cuda.current_device()
     return _call("int8_quant_channels", _ptr(w_f32, _f32t, d), G, N, K, _ptr(out_int8, _i8t, d),
-                 _ptr(scales, _f32t, d), _stream(stream))
+                 _ptr(scales, _f32t, d), _on(stream, d))
 
 
 def grouped_int8_gemm(A, A_scale, a_row_index, B, B_scale, group_offsets, G, M_total, N, K, C_bf16,
@@ -405,7 +410,7 @@ def grouped_int8_gemm(A, A_scale, a_row_index, B, B_scale, group_offsets, G, M_t
     return _call("grouped_int8_gemm", _ptr(A, _i8t, d), _ptr(A_scale, _f32t, d),
                  _ptr(a_row_index, _i32t, d), _rows(A), _ptr(B, _i8t, d), _ptr(B_scale, _f32t, d),
                  _ptr(group_offsets, _i32t, d), G, M_total, N, K, _ptr(C_bf16, _bf16t, d),
-                 _stream(stream))
+                 _on(stream, d))
 
 
 def grouped_int8_gemm_swiglu(A, A_scale, a_row_index, B, B_scale, group_offsets, G, M_total, I, K,
@@ -414,4 +419,4 @@ def grouped_int8_gemm_swiglu(A, A_scale, a_row_index, B, B_scale, group_offsets,
     return _call("grouped_int8_gemm_swiglu", _ptr(A, _i8t, d), _ptr(A_scale, _f32t, d),
                  _ptr(a_row_index, _i32t, d), _rows(A), _ptr(B, _i8t, d), _ptr(B_scale, _f32t, d),
                  _ptr(group_offsets, _i32t, d), G, M_total, I, K, _ptr(H_bf16, _bf16t, d),
-                 _stream(stream))
+                 _on(stream, d))
