@@ -853,6 +853,7 @@ extern "C" int moe_gate(const void* logits, int32_t logits_type, int64_t T, int3
                     ((uintptr_t)bias & 3) == 0 && ((uintptr_t)topk_idx & 3) == 0 &&
                     ((uintptr_t)topk_w & 3) == 0 && ((uintptr_t)scores & 3) == 0,
                 "moe_gate: tensors must be aligned to their elements");
+    MOE_INVALID(logits != scores, "moe_gate: logits and scores alias");
   }
   if (T == 0) {
     gate_zero_kernel<<<1, GT, 0, st>>>(expert_counts, E);

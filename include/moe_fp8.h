@@ -636,7 +636,7 @@ int moe_router_logits_backward(const void* x_bf16, const float* centroids, const
  * score           MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID
  * topk_idx  (out) [T, k] int32, ascending per row;  topk_w (out) [T, k] fp32
  * expert_counts (out) [E] int32
- * scores    (out, optional: NULL skips it) [T, E] fp32: s
+ * scores    (out, optional: NULL skips it) [T, E] fp32: s; not aliasing logits
  * Requirements: 1 <= E <= 1024; n_group <= 32 divides E; 1 <= topk_group <=
  * n_group; group_top in {1, 2}; 1 <= k <= 8; k <= topk_group * E / n_group;
  * scale finite; tensors aligned to their elements.

@@ -270,6 +270,7 @@ def test_gate_validation():
     assert g(logits=ctypes.c_void_p(4098)) == L.MOE_ERR_INVALID and "aligned" in L.last_error()
     assert g(scores=ctypes.c_void_p(4098)) == L.MOE_ERR_INVALID
     assert g(bias=ctypes.c_void_p(4097)) == L.MOE_ERR_INVALID
+    assert g(scores=FAKE) == L.MOE_ERR_INVALID and "alias" in L.last_error()
 
     def b(lt=0, T=4, E=64, score=0, k=4, rn=1, scale=1.0, idx=FAKE, dl=ctypes.c_void_p(8192), ds=None):
         return rc("moe_gate_backward", FAKE, lt, T, E, score, k, rn, scale, idx, FAKE, ds, dl, None)

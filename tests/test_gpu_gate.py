@@ -164,6 +164,27 @@ def test_gate_large_batch_and_empty():
     assert (counts == 0).all()
 
 
+def test_gate_more_tokens_than_a_grid_holds():
+    """A workgroup takes several rounds of tokens, some of which need the order
+    of 64 bits (equal scores + bias at the border) in each."""
+    T, E, k = 70001, 64, 6
+    rng = np.random.default_rng(8)
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    l[::5] = np.round(l[::5] * 2) / 2
+    logits, lh = as_logits(l, "f32")
+    bias = np.zeros(E, np.float32)
+    log("[gate] T=70001")
+    args = (OG.SOFTMAX, 8, 4, 2, k, 1, 1.0)
+    got = run_gate(logits, bias, *args)
+    assert np.array_equal(got[2], np.bincount(got[0].ravel(), minlength=E))
+    part = np.unique(np.concatenate([np.arange(0, T, 41), np.arange(65520, 65560), np.arange(T - 20, T)]))
+    ref = OG.gate(lh[part], bias, *args)
+    assert np.array_equal(got[0][part], ref["idx"])
+    # weights: as in check()
+    tol = 2 * score_bound(lh, OG.SOFTMAX) + (k + 3) * U
+    assert (np.abs(got[1][part] - ref["w"]) <= tol * ref["w"]).all()
+
+
 def run_backward(logits, score, k, renorm, scale, idx, dw, ds):
     T, E = logits.shape
     dl = torch.full((T, E), np.nan, dtype=logits.dtype, device="cuda")

@@ -240,3 +240,53 @@ def test_streams_and_graph_replay():
             check(bf16_values_host(outs[i]), refs[i], 4 * 2.0 ** -24, f"replay {rep}")
         call(rep % 2, None)
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("R,a_rows,N,K,gather", [
+    (1048700, 1048700, 8, 4096, False),    # rows of A past 2^32 bytes
+    (300, 1048700, 136, 4096, True),       # gathered from there
+    (20, 1048700, 24, 4096, True),
+    (1048700, 1048700, 2056, 144, False),  # the output past 2^32 bytes
+    (33560000, 1000, 64, 16, True),
+])
+def test_offsets_past_32_bits(R, a_rows, N, K, gather):
+    """Two groups, the second from an odd row on; sampled rows, the last ones
+    among them."""
+    log(f"[int8 far] R={R} A={a_rows} N={N} K={K} gather={gather}")
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    a = torch.randint(-127, 128, (a_rows, K), dtype=torch.int8, device="cuda", generator=gen)
+    b = torch.randint(-127, 128, (2, N, K), dtype=torch.int8, device="cuda", generator=gen)
+    sa = torch.rand((a_rows,), device="cuda", generator=gen) + 0.5
+    sb = torch.rand((2, N), device="cuda", generator=gen) + 0.5
+    index = None
+    if gather:
+        index = torch.randint(0, a_rows, (R,), dtype=torch.int32, device="cuda", generator=gen)
+        index[-7:] = a_rows - 1 - torch.arange(7, dtype=torch.int32, device="cuda")
+    cut = R // 2 + 1
+    out = torch.zeros((R, N), dtype=torch.bfloat16, device="cuda")
+    M.grouped_int8_gemm(a, sa, index, b, sb, dev(np.array([0, cut, R], np.int32)), 2, R, N, K, out)
+    rows = np.unique(np.concatenate([np.arange(0, R, max(1, R // 97)), np.arange(cut - 3, cut + 3),
+                                     np.arange(R - 9, R)]))
+    pick = torch.from_numpy(rows).cuda()
+    src = pick if index is None else index[pick].long()
+    offs = np.array([0, int((rows < cut).sum()), len(rows)], np.int32)
+    p = OI.products(host(a[src]), host(sa[src]), host(b), host(sb), offs)
+    check(bf16_values_host(out[pick].contiguous()), p, 4 * 2.0 ** -24, "gemm")
+    del a, out
+    torch.cuda.empty_cache()
+
+
+def test_quantised_rows_past_32_bits():
+    M_, K = 300_007, 8192   # 4.9 GB of bf16, 2.46 GB of codes
+    x = torch.empty((M_, K), dtype=torch.bfloat16, device="cuda")
+    pick = np.array([0, 1, 131071, 131072, 262143, 262144, M_ - 2, M_ - 1])
+    x.normal_(generator=torch.Generator(device="cuda").manual_seed(6))
+    q = torch.empty((M_, K), dtype=torch.int8, device="cuda")
+    s = torch.empty((M_,), device="cuda")
+    log(f"[int8 rows far] M={M_} K={K}")
+    M.int8_quant_rows(x, M_, K, K, q, s)
+    at = torch.from_numpy(pick).cuda()
+    rq, rs = OI.quant_rows(host(x[at].float()))
+    assert np.array_equal(host(s[at]), rs) and np.array_equal(host(q[at]), rq)
+    del x, q
+    torch.cuda.empty_cache()
