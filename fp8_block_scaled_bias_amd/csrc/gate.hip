@@ -37,6 +37,9 @@ struct GateArgs {
   const float* bias;
   int64_t T;
   int E, n_group, topk_group, group_top, k;
+  int size;        // of a group
+  int share;       // log2 of the lanes that look at one
+  uint32_t magic;  // e / size = e * magic >> 20 for e < 1024
   bool softmax, renorm;
   float scale;
   int32_t* topk_idx;
@@ -72,7 +75,15 @@ __device__ __forceinline__ int partner(int x) {
   if (R == 1) return __builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, true);
   if (R == 2) return __builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, true);
   if (R == 3) return __builtin_amdgcn_mov_dpp(x, 0x140, 0xF, 0xF, true);
-  return __shfl_xor(x, R == 4 ? 16 : 32, 64);
+  // rows (halves) exchanged between two registers: [0] has the even rows (the
+  // lower half) twice, [1] the odd ones (the upper half)
+  const int lane = threadIdx.x & 63;
+  if (R == 4) {
+    const auto r = __builtin_amdgcn_permlane16_swap((uint32_t)x, (uint32_t)x, false, false);
+    return (int)(lane & 16 ? r[0] : r[1]);
+  }
+  const auto r = __builtin_amdgcn_permlane32_swap((uint32_t)x, (uint32_t)x, false, false);
+  return (int)(lane & 32 ? r[0] : r[1]);
 }
 template <int R>
 __device__ __forceinline__ float partner(float v) { return __int_as_float(partner<R>(__float_as_int(v))); }
@@ -112,7 +123,7 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double*
                                            int* s_hist) {
   const int lane = threadIdx.x & 63;
   const D* row = static_cast<const D*>(a.logits) + t * a.E;
-  const int E = a.E, size = E / a.n_group;
+  const int E = a.E, size = a.size;
   float l[VPL], s[VPL], bias[VPL];
   double v[VPL];
   float m = -INFINITY;
@@ -160,20 +171,30 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double*
   }
   if (a.n_group > 1) {
     __builtin_amdgcn_wave_barrier();
-    if (lane < a.n_group) {
-      double t1 = -INFINITY, t2 = -INFINITY;
-      int at = lane < size ? lane : 0;  // each lane begins at a place of its own: other banks
+    // 2^sh lanes a group, every 2^sh-th expert each
+    int sh = 0;
+    while (sh < 3 && a.n_group << (sh + 1) <= 64) ++sh;
+    const int g = lane >> sh, part = lane & ((1 << sh) - 1);
+    double t1 = -INFINITY, t2 = -INFINITY;
+    auto take = [&](double x) {
+      t2 = fmax(t2, fmin(t1, x));
+      t1 = fmax(t1, x);
+    };
+    if (g < a.n_group) {
 #pragma unroll 4
-      for (int i = 0; i < size; ++i) {
-        const double x = s_v[lane * size + at];
-        at = at + 1 == size ? 0 : at + 1;
-        if (x > kExcluded) {
-          t2 = fmax(t2, fmin(t1, x));
-          t1 = fmax(t1, x);
-        }
+      for (int i = part; i < size; i += 1 << sh) {
+        const double x = s_v[g * size + i];
+        if (x > kExcluded) take(x);
       }
-      s_g[lane] = (a.group_top == 2 && t2 > -INFINITY) ? t1 + t2 : t1;
     }
+    auto meet2 = [&](double y1, double y2) {
+      take(y1);
+      t2 = fmax(t2, y2);
+    };
+    if (sh > 0) meet2(partner<0>(t1), partner<0>(t2));
+    if (sh > 1) meet2(partner<1>(t1), partner<1>(t2));
+    if (sh > 2) meet2(partner<2>(t1), partner<2>(t2));
+    if (g < a.n_group && part == 0) s_g[g] = (a.group_top == 2 && t2 > -INFINITY) ? t1 + t2 : t1;
     __builtin_amdgcn_wave_barrier();
     const double mine = s_g[lane < a.n_group ? lane : 0];
     int rank = 0;
@@ -184,7 +205,7 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double*
     const uint64_t kept = __ballot(lane < a.n_group && rank < a.topk_group);
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (i * 64 + lane < E && !((kept >> ((i * 64 + lane) / size)) & 1)) v[i] = -INFINITY;
+      if (i * 64 + lane < E && !((kept >> (((i * 64 + lane) * a.magic) >> 20)) & 1)) v[i] = -INFINITY;
   }
   // k times the largest that is left, the lowest id among equals
   uint32_t taken = 0;
@@ -328,6 +349,16 @@ __global__ __launch_bounds__(GT) void gate_kernel(GateArgs a) {
   const bool vec = (E & 3) == 0 && ((uintptr_t)a.logits & (4 * sizeof(D) - 1)) == 0;
   const bool vec_out = (E & 3) == 0 && ((uintptr_t)a.scores & 15) == 0;
   const int64_t step = (int64_t)gridDim.x * W * TPW, first = ((int64_t)blockIdx.x * W + wv) * TPW;
+  const int size = a.size;
+  // the bias waits in LDS, read while the first tokens' logits are on their way
+  __shared__ __attribute__((aligned(16))) float s_bias[EMAX];
+  if (a.bias) {
+    const float warm = load_logit(static_cast<const D*>(a.logits) + min(first + sub, a.T - 1) * E +
+                                  min((lane & (LPT - 1)) * V, E - 1));
+    for (int e = threadIdx.x; e < EMAX; e += GT) s_bias[e] = a.bias[min(e, E - 1)];
+    __syncthreads();
+    asm volatile("" ::"v"(warm));
+  }
   uint64_t any = 0;  // whether a token of this wave is left for the second look
   for (int64_t t0 = first; t0 < a.T; t0 += step) {
     const int64_t t = min(t0 + sub, a.T - 1);
@@ -402,9 +433,12 @@ __global__ __launch_bounds__(GT) void gate_kernel(GateArgs a) {
     const bool by_score = a.bias || a.group_top == 2;  // of the groups' values
     if (a.bias) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = 4 * (LPT * (i >> 2) + l) + (i & 3);
-        x[i] = x[i] == -INFINITY ? -INFINITY : s[i] + a.bias[min(e, E - 1)];
+      for (int c = 0; c < C; ++c) {
+        float b[4];
+        load4(s_bias + 4 * (LPT * c + l), b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          x[4 * c + j] = x[4 * c + j] == -INFINITY ? -INFINITY : s[4 * c + j] + b[j];
       }
     }
     if (a.n_group > 1) {
@@ -419,32 +453,42 @@ __global__ __launch_bounds__(GT) void gate_kernel(GateArgs a) {
         *reinterpret_cast<float4*>(v + 4 * (LPT * c + l)) = make_float4(y[0], y[1], y[2], y[3]);
       }
       __builtin_amdgcn_wave_barrier();
-      // lane g: the two largest of group g
-      const int size = E / a.n_group;
-      const float* mine_v = v + (l < a.n_group ? l : 0) * size;
+      // the two largest of each group: 2^sh lanes a group, every 2^sh-th of
+      // its experts (in fours) each
+      const int sh = a.share, g = l >> sh, part = l & ((1 << sh) - 1);
+      const float* mine_v = v + (g < a.n_group ? g : 0) * size;
       float t1 = -INFINITY, t2 = -INFINITY;
       auto take = [&](float y) {
         t2 = __builtin_amdgcn_fmed3f(t1, t2, y);  // t2 <= t1: the second largest of the three
         t1 = y > t1 ? y : t1;
       };
       if ((size & 3) == 0) {
-        const int n4 = size >> 2;
-        int at = l < n4 ? l : 0;  // each lane begins at a place of its own: other banks
+        const int n = ((size >> 2) - part + (1 << sh) - 1) >> sh;
+        int at = g < n ? g : 0;  // each group begins at a place of its own: other banks
 #pragma unroll 4
-        for (int i = 0; i < n4; ++i) {
-          const float4 y = *reinterpret_cast<const float4*>(mine_v + 4 * at);
+        for (int i = 0; i < n; ++i) {
+          const float4 y = *reinterpret_cast<const float4*>(mine_v + 4 * ((at << sh) + part));
           take(y.x); take(y.y); take(y.z); take(y.w);
-          at = at + 1 == n4 ? 0 : at + 1;
+          at = at + 1 == n ? 0 : at + 1;
         }
       } else {
 #pragma unroll 4
-        for (int i = 0; i < size; ++i) take(mine_v[i]);
+        for (int i = part; i < size; i += 1 << sh) take(mine_v[i]);
       }
-      const float worth = l >= a.n_group ? -INFINITY : a.group_top == 2 && t2 > -INFINITY ? t1 + t2 : t1;
+      auto meet2 = [&](float y1, float y2) {
+        take(y1);
+        t2 = y2 > t2 ? y2 : t2;
+      };
+      if (sh > 0) meet2(partner<0>(t1), partner<0>(t2));
+      if (sh > 1) meet2(partner<1>(t1), partner<1>(t2));
+      if (sh > 2) meet2(partner<2>(t1), partner<2>(t2));
       constexpr int GL = LPT == 64 ? GMAXG : 16;
       float* gs = reinterpret_cast<float*>(s_g[wv]) + 16 * sub;
-      if (l < GL) gs[l] = worth;
+      if (part == 0 && g < GL)
+        gs[g] = g >= a.n_group ? -INFINITY : a.group_top == 2 && t2 > -INFINITY ? t1 + t2 : t1;
+      if (sh > 0 && l < GL && l >= LPT >> sh) gs[l] = -INFINITY;
       __builtin_amdgcn_wave_barrier();
+      const float worth = gs[l < GL ? l : 0];
       const float near = by_score ? 2.f * err + 0x1p-21f * fabsf(worth) : 0.f;
       int rank = 0, close = 0;
 #pragma unroll
@@ -461,18 +505,17 @@ __global__ __launch_bounds__(GT) void gate_kernel(GateArgs a) {
       // (without scores equal groups are in their order already)
       redo = by_score && mine && close > a.topk_group;
       const uint32_t kept = (uint32_t)(__ballot(mine) >> (LPT == 64 ? 0 : 16 * sub));
-      const uint32_t magic = ((1u << 20) + size - 1) / size;  // e / size = e * magic >> 20 for e < 1024
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const uint32_t e = 4 * (LPT * c + l);
         if ((size & 3) == 0) {
-          const bool in = (kept >> ((e * magic) >> 20)) & 1;
+          const bool in = (kept >> ((e * a.magic) >> 20)) & 1;
 #pragma unroll
           for (int j = 0; j < 4; ++j) x[4 * c + j] = in ? x[4 * c + j] : -INFINITY;
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            x[4 * c + j] = (kept >> (((e + j) * magic) >> 20)) & 1 ? x[4 * c + j] : -INFINITY;
+            x[4 * c + j] = (kept >> (((e + j) * a.magic) >> 20)) & 1 ? x[4 * c + j] : -INFINITY;
         }
       }
     }
@@ -858,8 +901,11 @@ extern "C" int moe_gate(const void* logits, int32_t logits_type, int64_t T, int3
   if (T == 0) {
     gate_zero_kernel<<<1, GT, 0, st>>>(expert_counts, E);
   } else {
-    const GateArgs a{logits, bias, T, E, n_group, topk_group, group_top, k,
-                     score == MOE_SCORE_SOFTMAX, renormalize != 0, scale,
+    const int size = E / n_group, lanes = E > 256 || n_group > 16 ? 64 : 16;
+    int share = 0;
+    while (share < 3 && n_group << (share + 1) <= lanes) ++share;
+    const GateArgs a{logits, bias, T, E, n_group, topk_group, group_top, k, size, share,
+                     ((1u << 20) + (uint32_t)size - 1) / (uint32_t)size, score == MOE_SCORE_SOFTMAX, renormalize != 0, scale,
                      topk_idx, topk_w, expert_counts, scores};
     if (logits_type == MOE_TYPE_F32) launch_gate<float>(a, st);
     else launch_gate<uint16_t>(a, st);
