@@ -41,15 +41,23 @@ __global__ __launch_bounds__(ST) void split_kernel(Args a) {
   const int nkb = (int)((K + 127) >> 7);
   const int64_t ntiles = (N + 16 * NO - 1) / (16 * NO);
   const int64_t b_rows = SWIGLU ? 2 * N : N;
-  build_group_tables<ST, 16 * MB>(a.offs, a.G, s_offs, s_pref, s_red, &s_carry);
-  const int64_t total = (int64_t)s_pref[a.G] * ntiles;
+  // one group whose rows fit a tile: the loads need not wait for its offsets
+  const bool lone = a.G == 1 && a.M_total <= 16 * MB;
+  if (!lone) build_group_tables<ST, 16 * MB>(a.offs, a.G, s_offs, s_pref, s_red, &s_carry);
+  const int64_t total = lone ? ntiles : (int64_t)s_pref[a.G] * ntiles;
   // an XCD's workgroups (blockIdx % 8) take a contiguous range of tiles, the
   // row tiles of one weight panel next to each other
   const int nper = gridDim.x >> 3;
   const int64_t chunk = (total + 7) >> 3;
   const int64_t lo = (blockIdx.x & 7) * chunk, hi = min(total, lo + chunk);
   for (int64_t L = lo + (blockIdx.x >> 3); L < hi; L += nper) {
-    gemm::Tile t = decode_tile(s_pref, s_offs, a.G, ntiles, L, 16 * MB);
+    gemm::Tile t{};
+    if (lone) {
+      t.nt = L;
+      t.m1 = (int)a.M_total;
+    } else {
+      t = decode_tile(s_pref, s_offs, a.G, ntiles, L, 16 * MB);
+    }
     const int g = __builtin_amdgcn_readfirstlane(t.g);
     const int m0 = __builtin_amdgcn_readfirstlane(t.m0), m1 = __builtin_amdgcn_readfirstlane(t.m1);
     const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane((int)t.nt) * (16 * NO);
@@ -129,7 +137,7 @@ __global__ __launch_bounds__(ST) void split_kernel(Args a) {
             for (int r = 0; r < 4; ++r) red[wv][4 * q + r][16 * j + r16] = acc[ii][j][r];
       __syncthreads();
       const int lr = tid >> 4, row = m0 + 16 * i + lr, c0 = (tid & 15) * NO;
-      if (row >= m1 || n0 + c0 >= N) continue;
+      if (row >= (lone ? a.offs[1] : m1) || n0 + c0 >= N) continue;
       const int64_t sr = a.index ? (int64_t)min((uint32_t)a.index[row], (uint32_t)(a.A_rows - 1)) : row;
       const float sa = a.sa[sr];
       const float* sb = a.sb + (int64_t)g * b_rows + n0;

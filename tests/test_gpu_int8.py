@@ -290,3 +290,19 @@ def test_quantised_rows_past_32_bits():
     assert np.array_equal(host(s[at]), rs) and np.array_equal(host(q[at]), rq)
     del x, q
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("rows,behind", [(0, 3), (1, 0), (1, 15), (16, 0), (9, 30), (60, 4)])
+@pytest.mark.parametrize("gather", [False, True])
+def test_one_group_of_few_rows(rows, behind, gather):
+    """One group (a linear layer) whose rows fit a tile, with rows behind it."""
+    N, K = 272, 400
+    log(f"[int8 one group] {rows}+{behind} gather={gather}")
+    c = case([rows], N, K, [rows, behind], gather, extra_rows=behind)
+    p = OI.products(c[1], c[3], c[2], c[4], c[0], c[5])
+    out = run(M.grouped_int8_gemm, *c, rows + behind, N, K)
+    check(bf16_values_host(out)[:rows], p, 4 * 2.0 ** -24, "gemm")
+    assert (host(out.view(torch.int16))[rows:] == 0x4321).all()
+    out = run(M.grouped_int8_gemm_swiglu, *c, rows + behind, N // 2, K)
+    check_swiglu(bf16_values_host(out)[:rows], p, "swiglu")
+    assert (host(out.view(torch.int16))[rows:] == 0x4321).all()
