@@ -4,7 +4,9 @@
 //   s = max |v| * fp32(1 / 127) (1 if that is 0),  code = v / s rounded to the
 //   nearest whole number (ties to even), from the exact quotient
 //
-// HBM bound: 2 B (bf16) or 4 B (fp32) in and 1 B out per element.
+// HBM bound: 2 B (bf16) or 4 B (fp32) in and 1 B out per element.  Measured:
+// 147456 x 2048 bf16 159 us (5.7 TB/s), 135168 x 7168 fp32 897 us (5.4 TB/s),
+// 128 x 7168 bf16 5.2 us.
 #include "common.h"
 
 namespace moe {

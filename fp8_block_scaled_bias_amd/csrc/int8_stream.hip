@@ -9,10 +9,13 @@
 // ahead.
 //  * flow_kernel, where there are tiles enough for every wave: each wave works
 //    on tiles of its own, 16 MB rows x 64 weight rows over the whole of K, and
-//    its loads run on from tile to tile.
+//    its loads run on from tile to tile.  256 groups of 4 rows, N = 7168, K =
+//    2048 (3.76 GB of weights): 635 us, 5.9 TB/s.
 //  * split_kernel, where there are not: a workgroup of four waves takes 16 MB
 //    rows x 16 NJ weight rows, its waves every fourth K block; their sums meet
-//    in LDS (whole numbers: the order does not matter).
+//    in LDS (whole numbers: the order does not matter).  One row, N = 4096, K =
+//    7168 (29 MB): 8.7 us, most of it the launch and the first loads' latency;
+//    10 or 14 blocks ahead instead of 6: 10.3 and 9.9 us.
 #include "int8_common.h"
 
 namespace moe {
