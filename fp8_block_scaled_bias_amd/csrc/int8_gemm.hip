@@ -39,15 +39,15 @@ int int8_gemm(const char* who, bool swiglu, const int8_t* A, const float* A_scal
   // The kernel by the rows of a group of average size (the host does not know
   // the groups' own) and by how many tiles there are for the CUs.  Times on
   // 64 groups, N = 4096, K = 7168 (wide / mid / stream): 8 rows 351 / 360 /
-  // 317 us, 16: 352 / 360 / 327, 32: 360 / 362 / 385, 128: 420 / 441 / 881;
-  // on one group: 16 rows 63 / 38 / 13 us, 64: 63 / 39 / 25, 256: 63 / 42 / 88,
-  // 1024: 65 / 45 / 108.
+  // 317 us, 16: 352 / 360 / 327, 32: 360 / 362 / 374, 128: 420 / 441 / 828;
+  // on one group: 16 rows 63 / 38 / 9 us, 64: 63 / 39 / 19, 256: 63 / 41 / 30
+  // (256 tiles of 64 x 64), 1024: 65 / 45 / 105.
   const int64_t avg = M_total / G, cus = gemm::num_cus();
   const int64_t cols = swiglu ? 2 * N : N;
   const int64_t wide_tiles = G * ceil_div(avg, 256) * ceil_div(cols, 256);
-  const int64_t mid_tiles = G * ceil_div(avg, 128) * ceil_div(cols, 128);
+  const int64_t small_tiles = G * ceil_div(avg, 64) * ceil_div(cols, 64);
   const bool fits = !a_row_index || A_rows * K < 0xFFF00000ll;  // 32-bit offsets into a gathered A
-  if (!fits || avg <= 16 || (avg <= 64 && mid_tiles < cus / 4)) launch_stream(a, swiglu, st);
+  if (!fits || avg <= 16 || small_tiles <= cus) launch_stream(a, swiglu, st);
   else if (K > 128 && wide_tiles >= cus) launch_wide(a, swiglu, st);
   else launch_mid(a, swiglu, st);
   return check_launch(who);

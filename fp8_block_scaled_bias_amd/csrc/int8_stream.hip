@@ -13,9 +13,11 @@
 //    2048 (3.76 GB of weights): 635 us, 5.9 TB/s.
 //  * split_kernel, where there are not: a workgroup of four waves takes 16 MB
 //    rows x 16 NJ weight rows, its waves every fourth K block; their sums meet
-//    in LDS (whole numbers: the order does not matter).  One row, N = 4096, K =
-//    7168 (29 MB): 8.7 us, most of it the launch and the first loads' latency;
-//    10 or 14 blocks ahead instead of 6: 10.3 and 9.9 us.
+//    in LDS (whole numbers: the order does not matter).  The K loop's end reads
+//    nothing past it: with the last block read again for every block ahead
+//    that is not there, one row of N = 16384, K = 4096 took 21 us instead of
+//    12.  One row, N = 4096, K = 7168 (29 MB): 7.6 us, most of it the launch
+//    and the first loads' latency; 64 rows 19.4 us.
 #include "int8_common.h"
 
 namespace moe {
@@ -31,12 +33,12 @@ constexpr int ST = 256;
 template <int NJ, int MB, int D, bool SWIGLU>
 __global__ __launch_bounds__(ST) void split_kernel(Args a) {
   constexpr int NO = SWIGLU ? NJ / 2 : NJ;  // 16-column blocks of the output
-  constexpr int PITCH = 16 * NJ + 4;
+  constexpr int W = ST / 64, PITCH = 16 * NJ + 4;
   __shared__ int s_offs[MAXG + 1];
   __shared__ int s_pref[MAXG + 1];
-  __shared__ int s_red[4];
+  __shared__ int s_red[W];
   __shared__ int s_carry;
-  __shared__ __attribute__((aligned(16))) int red[4][16][PITCH];
+  __shared__ __attribute__((aligned(16))) int red[W][16][PITCH];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, q = lane >> 4;
@@ -119,12 +121,21 @@ __global__ __launch_bounds__(ST) void split_kernel(Args a) {
               acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xa[i][h], xb[j][h], acc[i][j], 0, 0, 0);
     };
 #pragma unroll
-    for (int d = 0; d < D - 1; ++d) load(fa[d], fb[d], min(wv + 4 * d, nkb - 1));
-    for (int kb = wv; kb < nkb; kb += 4 * D) {
+    for (int d = 0; d < D - 1; ++d)
+      if (wv + W * d < nkb) load(fa[d], fb[d], wv + W * d);
+    int kb = wv;
+    for (; kb + 2 * W * (D - 1) < nkb; kb += W * D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        const int cur = kb + 4 * d;
-        load(fa[(d + D - 1) % D], fb[(d + D - 1) % D], min(cur + 4 * (D - 1), nkb - 1));
+        load(fa[(d + D - 1) % D], fb[(d + D - 1) % D], kb + W * (d + D - 1));
+        multiply(fa[d], fb[d], kb + W * d);
+      }
+    }
+    for (; kb < nkb; kb += W * D) {  // the last blocks: nothing is read twice
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        const int cur = kb + W * d, next = cur + W * (D - 1);
+        if (next < nkb) load(fa[(d + D - 1) % D], fb[(d + D - 1) % D], next);
         if (cur < nkb) multiply(fa[d], fb[d], cur);
       }
     }
@@ -329,7 +340,11 @@ void launch(const Args& a, int64_t tiles, hipStream_t st) {
 
 template <bool SWIGLU>
 void dispatch(const Args& a, hipStream_t st) {
-  // row tiles: at least this many in groups of equal size, at most that many
+  // Row tiles by the groups' average size.  Wider column tiles read a token's
+  // row for more weights, narrower ones are more: the widest that still gives
+  // every CU one (16 to 64 rows; one group of 30, N = 16384, K = 4096: 14.5 us
+  // with 64 columns, 24.5 with 16; of 64, N = 4096, K = 7168: 22.4 us with 32,
+  // 19.4 with 16) or two.
   const int64_t avg = a.M_total / a.G;
   const int64_t m16 = std::min<int64_t>(a.M_total, a.G + a.M_total / 16);
   const int64_t n64 = ceil_div(a.N, SWIGLU ? 32 : 64);
@@ -338,11 +353,13 @@ void dispatch(const Args& a, hipStream_t st) {
   if (avg <= 16) {
     if (m16 * n64 >= 4 * few) launch_flow<1, 3, SWIGLU>(a, st);
     else if (m16 * n64 >= few) launch<4, 1, 3, SWIGLU>(a, m16 * n64, st);
-    else launch<N1, 1, 6, SWIGLU>(a, m16 * ceil_div(a.N, 16), st);
+    else launch<N1, 1, 3, SWIGLU>(a, m16 * ceil_div(a.N, 16), st);
   } else {
-    const int64_t m64 = std::min<int64_t>(a.M_total, a.G + a.M_total / 64);
-    if (m64 * n64 >= few) launch<4, 4, 2, SWIGLU>(a, m64 * n64, st);
-    else launch<N1, 4, 4, SWIGLU>(a, m64 * ceil_div(a.N, 16), st);
+    const int64_t m64 = a.G * ceil_div(avg, 64);
+    const int64_t n32 = ceil_div(a.N, 32), cus = gemm::num_cus();
+    if (m64 * n64 >= cus) launch<4, 4, 2, SWIGLU>(a, m64 * n64, st);
+    else if (!SWIGLU && m64 * n32 >= cus) launch<2, 4, 3, SWIGLU>(a, m64 * n32, st);
+    else launch<N1, 4, 3, SWIGLU>(a, m64 * ceil_div(a.N, 16), st);
   }
 }
 
