@@ -306,3 +306,17 @@ def test_one_group_of_few_rows(rows, behind, gather):
     out = run(M.grouped_int8_gemm_swiglu, *c, rows + behind, N // 2, K)
     check_swiglu(bf16_values_host(out)[:rows], p, "swiglu")
     assert (host(out.view(torch.int16))[rows:] == 0x4321).all()
+
+
+@pytest.mark.parametrize("M_,K", [(300, 4096), (256, 4096), (512, 8192), (513, 7168), (513, 8200), (512, 16384),
+                                  (2048, 520), (2051, 2048), (2047, 1024)])
+def test_quant_rows_by_every_number_of_waves(M_, K):
+    """Rows by one wave, four and sixteen, at both sides of each border."""
+    rng = np.random.default_rng([M_, K])
+    bits = bf16_bits(np.concatenate([hard_rows(K, rng), rng.standard_normal((M_ - 8, K)).astype(np.float32)]))
+    q = torch.full((M_, K), 99, dtype=torch.int8, device="cuda")
+    s = torch.full((M_,), -1.0, device="cuda")
+    log(f"[int8 rows] M={M_} K={K}")
+    M.int8_quant_rows(bf16_dev(bits), M_, K, K, q, s)
+    rq, rs = OI.quant_rows(bf16_value_from_bits(bits).astype(np.float32))
+    assert np.array_equal(host(s), rs) and np.array_equal(host(q), rq)
