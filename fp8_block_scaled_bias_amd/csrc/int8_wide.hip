@@ -17,7 +17,7 @@
 //    its MFMAs a phase reads the operands that the next one adds (B1, A1,
 //    then A0 and B0 of the next K block), and copies into the region that
 //    the phase before read, for the K block after the next: a copy has six
-//    phases, 3072 clocks, to land.  A barrier ends each phase; the last MFMA
+//    phases, a K block and a half, to land.  A barrier ends each phase; the last MFMA
 //    covers it.
 //  * Copies run on across tiles: the next tile's first two K blocks load
 //    while the last ones of this tile are multiplied.
