@@ -153,7 +153,7 @@ def _rows(t):
 
 
 def _call(name, *args):
-    rc = getattr(lib(), name)(*args)
+    rc = getattr(_lib or lib(), name)(*args)
     if rc != MOE_OK:
         raise MoEError(name, rc, last_error())
     return rc
@@ -330,6 +330,8 @@ def moe_combine(expert_out_bf16, inv_perm, topk_w, shared_out_bf16, T, k, H, y_b
 
 
 _f32t, _bf16t, _i32t, _i8t = torch.float32, torch.bfloat16, torch.int32, torch.int8
+_Tensor, _device = torch.Tensor, torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (not in a torch without GPUs)
 
 
 def _ptr(t, dtype, dev):
@@ -337,7 +339,7 @@ def _ptr(t, dtype, dev):
     GPU `dev`, where the call's kernels run (None -> NULL).  dtype None: any."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"expected a torch.Tensor, got {type(t)}")
     if t.get_device() != dev or not t.is_contiguous() or (dtype is not None and t.dtype is not dtype):
         if t.is_cuda and t.get_device() != dev:
@@ -349,24 +351,24 @@ def _ptr(t, dtype, dev):
 
 def _on(stream, dev):
     """_stream, with the current stream's handle taken directly."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    return _raw_stream(dev) if stream is None else _stream(stream)
 
 
 def _logits_type(t):
-    if not isinstance(t, torch.Tensor) or t.dtype not in (_f32t, _bf16t):
+    if not isinstance(t, _Tensor) or t.dtype not in (_f32t, _bf16t):
         raise TypeError("logits must be a float32 or bfloat16 torch.Tensor")
     return TYPE_F32 if t.dtype == _f32t else TYPE_BF16
 
 
 def moe_router_logits(x_bf16, T, H, centroids, E, logits, workspace, workspace_bytes, stream=None):
-    d = torch.cuda.current_device()
+    d = _device()
     return _call("moe_router_logits", _ptr(x_bf16, _bf16t, d), T, H, _ptr(centroids, _f32t, d), E,
                  _ptr(logits, _f32t, d), _ptr(workspace, None, d), workspace_bytes, _on(stream, d))
 
 
 def moe_router_logits_backward(x_bf16, centroids, d_logits, T, H, E, dx_in_bf16, dx_out_bf16,
                                d_centroids, workspace, workspace_bytes, stream=None):
-    d = torch.cuda.current_device()
+    d = _device()
     return _call("moe_router_logits_backward", _ptr(x_bf16, _bf16t, d), _ptr(centroids, _f32t, d),
                  _ptr(d_logits, _f32t, d), T, H, E, _ptr(dx_in_bf16, _bf16t, d),
                  _ptr(dx_out_bf16, _bf16t, d), _ptr(d_centroids, _f32t, d), _ptr(workspace, None, d),
@@ -375,7 +377,7 @@ def moe_router_logits_backward(x_bf16, centroids, d_logits, T, H, E, dx_in_bf16,
 
 def moe_gate(logits, T, E, bias, score, n_group, topk_group, group_top, k, renormalize, scale,
              topk_idx, topk_w, expert_counts, stream=None, *, scores=None):
-    d = torch.cuda.current_device()
+    d = _device()
     kind = _logits_type(logits)
     return _call("moe_gate", _ptr(logits, None, d), kind, T, E, _ptr(bias, _f32t, d), score, n_group,
                  topk_group, group_top, k, int(renormalize), scale, _ptr(topk_idx, _i32t, d),
@@ -385,7 +387,7 @@ def moe_gate(logits, T, E, bias, score, n_group, topk_group, group_top, k, renor
 
 def moe_gate_backward(logits, T, E, score, k, renormalize, scale, topk_idx, d_topk_w, d_logits,
                       stream=None, *, d_scores=None):
-    d = torch.cuda.current_device()
+    d = _device()
     kind = _logits_type(logits)
     return _call("moe_gate_backward", _ptr(logits, None, d), kind, T, E, score, k, int(renormalize),
                  scale, _ptr(topk_idx, _i32t, d), _ptr(d_topk_w, _f32t, d), _ptr(d_scores, _f32t, d),
@@ -393,20 +395,20 @@ def moe_gate_backward(logits, T, E, score, k, renormalize, scale, topk_idx, d_to
 
 
 def int8_quant_rows(in_bf16, M, K, ld_in, out_int8, scales, stream=None):
-    d = torch.cuda.current_device()
+    d = _device()
     return _call("int8_quant_rows", _ptr(in_bf16, _bf16t, d), M, K, ld_in, _ptr(out_int8, _i8t, d),
                  _ptr(scales, _f32t, d), _on(stream, d))
 
 
 def int8_quant_channels(w_f32, G, N, K, out_int8, scales, stream=None):
-    d = torch.cuda.current_device()
+    d = _device()
     return _call("int8_quant_channels", _ptr(w_f32, _f32t, d), G, N, K, _ptr(out_int8, _i8t, d),
                  _ptr(scales, _f32t, d), _on(stream, d))
 
 
 def grouped_int8_gemm(A, A_scale, a_row_index, B, B_scale, group_offsets, G, M_total, N, K, C_bf16,
                       stream=None):
-    d = torch.cuda.current_device()
+    d = _device()
     return _call("grouped_int8_gemm", _ptr(A, _i8t, d), _ptr(A_scale, _f32t, d),
                  _ptr(a_row_index, _i32t, d), _rows(A), _ptr(B, _i8t, d), _ptr(B_scale, _f32t, d),
                  _ptr(group_offsets, _i32t, d), G, M_total, N, K, _ptr(C_bf16, _bf16t, d),
@@ -415,7 +417,7 @@ def grouped_int8_gemm(A, A_scale, a_row_index, B, B_scale, group_offsets, G, M_t
 
 def grouped_int8_gemm_swiglu(A, A_scale, a_row_index, B, B_scale, group_offsets, G, M_total, I, K,
                              H_bf16, stream=None):
-    d = torch.cuda.current_device()
+    d = _device()
     return _call("grouped_int8_gemm_swiglu", _ptr(A, _i8t, d), _ptr(A_scale, _f32t, d),
                  _ptr(a_row_index, _i32t, d), _rows(A), _ptr(B, _i8t, d), _ptr(B_scale, _f32t, d),
                  _ptr(group_offsets, _i32t, d), G, M_total, I, K, _ptr(H_bf16, _bf16t, d),
