@@ -37,6 +37,7 @@
 // N = 7168, K = 2048 in 1.84 ms, 2.1 POP/s (65 %, 1.53 GHz); the same with
 // SwiGLU, I = 2048, K = 7168, gathered, in 3.34 ms, 2.3 POP/s.
 #include "int8_common.h"
+#include "int8_wide_waits.h"
 
 namespace moe {
 namespace int8 {
@@ -375,18 +376,18 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
     copy_region(ic<1>(), s);
     if (s == 0) copy_next();
   }
-  wait_copies<24>();
+  wait_copies<waits::prologue(0)>();
   barrier();
 #pragma unroll
   for (int n = 0; n < 8; ++n) {
     read_one(ic<0>(), n, 0);
     read_one(ic<2>(), n, 0);
   }
-  wait_copies<24>();
+  wait_copies<waits::prologue(1)>();
   barrier();
   copy_next();
   copy_region(ic<0>(), 0);  // A0 of the third
-  wait_copies<24>();
+  wait_copies<waits::prologue(2)>();
   barrier();
 
   // A phase: MFMAs of A half H and B half B; reads region R of stage rst for
@@ -428,10 +429,8 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
     barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
-  // Ends of phases: the phase's reads are in registers; the copies that the
-  // next phase reads have landed, after which six phases of four copies were
-  // issued, and in the epilogue's four phases S0, S1, S0, S1 stores.
-  constexpr int S1 = SWIGLU ? 6 : 10, S0 = 2 * NE - S1;
+  // Ends of phases: the phase's reads are in registers, the copies that the
+  // next phase reads have landed (int8_wide_waits.h).
   uint32_t st = 0;  // stage of the K block being multiplied
   Done done{t, 0};  // the tile before, whose A1 is still to be stored
   done.t.rows = 0;
@@ -440,18 +439,18 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
     if (FIRST) scale_copy();
     if (LAST && tail) clear_tail(ic<0>());
     phase(ic<0>(), ic<0>(), ic<3>(), st, ic<2>(), st, FIRST_, ic<(FIRST ? 0 : -1)>(),
-          ic<24 + (FIRST ? 2 * S0 + S1 : 0)>(), done);
+          ic<waits::phase(SWIGLU, FIRST, LAST, 0)>(), done);
     phase(ic<0>(), ic<1>(), ic<1>(), st, ic<3>(), st, FIRST_, ic<(FIRST ? 1 : -1)>(),
-          ic<24 + (FIRST ? 2 * S0 + 2 * S1 : 0)>(), done);
+          ic<waits::phase(SWIGLU, FIRST, LAST, 1)>(), done);
     if (LAST) {
       if (tail) clear_tail(ic<1>());
       done = Done{t, to & 1};
     }
     phase(ic<1>(), ic<0>(), ic<0>(), st ^ 1, ic<1>(), st, FIRST_, ic<(LAST ? 0 : -1)>(),
-          ic<24 + (FIRST ? 2 * S0 + 2 * S1 : LAST ? S0 : 0)>(), done);
+          ic<waits::phase(SWIGLU, FIRST, LAST, 2)>(), done);
     copy_next();
     phase(ic<1>(), ic<1>(), ic<2>(), st ^ 1, ic<0>(), st ^ 1, FIRST_, ic<(LAST ? 1 : -1)>(),
-          ic<24 + (FIRST ? 2 * S0 + 2 * S1 : LAST ? S0 + S1 : 0)>(), done);
+          ic<waits::phase(SWIGLU, FIRST, LAST, 3)>(), done);
     st ^= 1;
   };
   for (; to < my_n; t = tile_at(t_g, ++to)) {
