@@ -2,6 +2,7 @@
 #pragma once
 
 #include "gemm_common.h"
+#include "int8_plan.h"
 
 namespace moe {
 namespace int8 {
@@ -35,7 +36,7 @@ void launch_wide(const Args& a, bool swiglu, hipStream_t st);
 void launch_mid(const Args& a, bool swiglu, hipStream_t st);
 
 // The weights straight into registers (int8_stream.hip): any size.
-void launch_stream(const Args& a, bool swiglu, hipStream_t st);
+void launch_stream(const Args& a, Plan p, bool swiglu, hipStream_t st);
 
 }  // namespace int8
 }  // namespace moe

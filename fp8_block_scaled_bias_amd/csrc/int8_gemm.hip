@@ -36,20 +36,10 @@ int int8_gemm(const char* who, bool swiglu, const int8_t* A, const float* A_scal
               "%s: A, B and the output must be 16-byte aligned, scales and indices 4-byte", who);
   const Args a{A, A_scale, a_row_index, A_rows, B, B_scale, group_offsets, G, M_total, N, K,
                    static_cast<uint16_t*>(C)};
-  // The kernel by the rows of a group of average size (the host does not know
-  // the groups' own) and by how many tiles there are for the CUs.  Times on
-  // 64 groups, N = 4096, K = 7168 (wide / mid / stream): 8 rows 351 / 360 /
-  // 317 us, 16: 352 / 360 / 327, 32: 360 / 362 / 374, 128: 420 / 441 / 828;
-  // on one group: 16 rows 63 / 38 / 9 us, 64: 63 / 39 / 19, 256: 63 / 41 / 30
-  // (256 tiles of 64 x 64), 1024: 65 / 45 / 105.
-  const int64_t avg = M_total / G, cus = gemm::num_cus();
-  const int64_t cols = swiglu ? 2 * N : N;
-  const int64_t wide_tiles = G * ceil_div(avg, 256) * ceil_div(cols, 256);
-  const int64_t small_tiles = G * ceil_div(avg, 64) * ceil_div(cols, 64);
-  const bool fits = !a_row_index || A_rows * K < 0xFFF00000ll;  // 32-bit offsets into a gathered A
-  if (!fits || avg <= 16 || small_tiles <= cus) launch_stream(a, swiglu, st);
-  else if (K > 128 && wide_tiles >= cus) launch_wide(a, swiglu, st);
-  else launch_mid(a, swiglu, st);
+  const Plan p = plan(Shape{swiglu, a_row_index != nullptr, A_rows, G, M_total, N, K}, gemm::num_cus());
+  if (p == kWide) launch_wide(a, swiglu, st);
+  else if (p == kMid) launch_mid(a, swiglu, st);
+  else launch_stream(a, p, swiglu, st);
   return check_launch(who);
 }
 

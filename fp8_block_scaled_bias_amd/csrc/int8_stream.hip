@@ -339,35 +339,24 @@ void launch(const Args& a, int64_t tiles, hipStream_t st) {
 }
 
 template <bool SWIGLU>
-void dispatch(const Args& a, hipStream_t st) {
-  // Row tiles by the groups' average size.  Wider column tiles read a token's
-  // row for more weights, narrower ones are more: the widest that still gives
-  // every CU one (16 to 64 rows; one group of 30, N = 16384, K = 4096: 14.5 us
-  // with 64 columns, 24.5 with 16; of 64, N = 4096, K = 7168: 22.4 us with 32,
-  // 19.4 with 16) or two.
-  const int64_t avg = a.M_total / a.G;
-  const int64_t m16 = std::min<int64_t>(a.M_total, a.G + a.M_total / 16);
-  const int64_t n64 = ceil_div(a.N, SWIGLU ? 32 : 64);
+void dispatch(const Args& a, Plan p, hipStream_t st) {
+  const Shape s{SWIGLU, a.index != nullptr, a.A_rows, a.G, a.M_total, a.N, a.K};
   constexpr int N1 = SWIGLU ? 2 : 1;
-  const int64_t few = 2 * gemm::num_cus();
-  if (avg <= 16) {
-    if (m16 * n64 >= 4 * few) launch_flow<1, 3, SWIGLU>(a, st);
-    else if (m16 * n64 >= few) launch<4, 1, 3, SWIGLU>(a, m16 * n64, st);
-    else launch<N1, 1, 3, SWIGLU>(a, m16 * ceil_div(a.N, 16), st);
-  } else {
-    const int64_t m64 = a.G * ceil_div(avg, 64);
-    const int64_t n32 = ceil_div(a.N, 32), cus = gemm::num_cus();
-    if (m64 * n64 >= cus) launch<4, 4, 2, SWIGLU>(a, m64 * n64, st);
-    else if (!SWIGLU && m64 * n32 >= cus) launch<2, 4, 3, SWIGLU>(a, m64 * n32, st);
-    else launch<N1, 4, 3, SWIGLU>(a, m64 * ceil_div(a.N, 16), st);
+  switch (p) {
+    case kFlow: return launch_flow<1, 3, SWIGLU>(a, st);
+    case kSplit16x64: return launch<4, 1, 3, SWIGLU>(a, m16(s) * n64(s), st);
+    case kSplit16x16: return launch<N1, 1, 3, SWIGLU>(a, m16(s) * n16(s), st);
+    case kSplit64x64: return launch<4, 4, 2, SWIGLU>(a, m64(s) * n64(s), st);
+    case kSplit64x32: return launch<2, 4, 3, SWIGLU>(a, m64(s) * n32(s), st);
+    default: return launch<N1, 4, 3, SWIGLU>(a, m64(s) * n16(s), st);
   }
 }
 
 }  // namespace
 
-void launch_stream(const Args& a, bool swiglu, hipStream_t st) {
-  if (swiglu) dispatch<true>(a, st);
-  else dispatch<false>(a, st);
+void launch_stream(const Args& a, Plan p, bool swiglu, hipStream_t st) {
+  if (swiglu) dispatch<true>(a, p, st);
+  else dispatch<false>(a, p, st);
 }
 
 }  // namespace int8
