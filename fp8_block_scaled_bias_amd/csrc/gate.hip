@@ -494,7 +494,12 @@ __global__ __launch_bounds__(GT) void gate_kernel(GateArgs a) {
       if (sh > 0 && l < GL && l >= LPT >> sh) gs[l] = -INFINITY;
       __builtin_amdgcn_wave_barrier();
       const float worth = gs[l < GL ? l : 0];
-      const float near = by_score ? 2.f * err + 0x1p-21f * fabsf(worth) : 0.f;
+      // the sums' roundings go by their parts, which may cancel: those of the
+      // two groups compared are under 2^-22 of the token's largest |t1| + |t2|
+      const bool two = a.group_top == 2 && t2 > -INFINITY;
+      const float parts = (t1 > -INFINITY ? fabsf(t1) : 0.f) + (two ? fabsf(t2) : 0.f);
+      const float near =
+          by_score ? 2.f * err + 0x1p-21f * __int_as_float(row_max<LPT>(__float_as_int(parts))) : 0.f;
       int rank = 0, close = 0;
 #pragma unroll
       for (int j = 0; j < GL; j += 4) {
@@ -503,7 +508,7 @@ __global__ __launch_bounds__(GT) void gate_kernel(GateArgs a) {
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           rank += (y[h] > worth || (y[h] == worth && j + h < l)) ? 1 : 0;
-          close += y[h] >= worth - near ? 1 : 0;
+          close += y[h] < worth - near ? 0 : 1;  // (infinite values: close)
         }
       }
       const bool mine = l < a.n_group && rank < a.topk_group;
