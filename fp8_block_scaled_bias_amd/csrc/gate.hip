@@ -326,6 +326,14 @@ __device__ __forceinline__ float sigmoid_f32(float l) {
   y = fmaf(fmaf(-d, y, 1.0f), y, y);
   return l >= 0.f ? y : z * y;
 }
+// its slope, s (1 - s) = z / (1 + z)^2 with z = exp(-|l|): 1 - s of a rounded s
+// has no bits left where s is near 1.  Relative error 9 roundings at any l.
+__device__ __forceinline__ float sigmoid_slope(float l) {
+  const float z = expf(-fabsf(l)), d = 1.0f + z;
+  float y = __builtin_amdgcn_rcpf(d);
+  y = fmaf(fmaf(-d, y, 1.0f), y, y);
+  return z * y * y;
+}
 // exp(l - m), relative error (2.2 |l - m| + 2) roundings
 __device__ __forceinline__ float exp_from(float l, float m) {
   return __builtin_amdgcn_exp2f((l - m) * 1.4426950408889634f);
@@ -720,7 +728,7 @@ __global__ __launch_bounds__(GT) void gate_backward_kernel(GateBwdArgs a) {
   D* out = static_cast<D*>(a.dl) + t * E;
   const bool vec = (E & 3) == 0 && (((uintptr_t)a.logits | (uintptr_t)a.dl) & (4 * sizeof(D) - 1)) == 0 &&
                    ((uintptr_t)a.ds & 15) == 0;
-  float s[V], g[V];
+  float s[V], g[V];  // logits, then softmax scores or the sigmoids' slopes; ds, then dl
 #pragma unroll
   for (int i = 0; i < V; ++i) g[i] = 0.f;
   if (vec) {
@@ -776,7 +784,7 @@ __global__ __launch_bounds__(GT) void gate_backward_kernel(GateBwdArgs a) {
     for (int i = 0; i < V; ++i) s[i] *= inv;
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = sigmoid_f32(s[i]);
+    for (int i = 0; i < V; ++i) s[i] = sigmoid_slope(s[i]);
   }
   // the choices' gradients (lanes 0..15 of a token; k <= 8)
   float val = dwj;
@@ -816,7 +824,7 @@ __global__ __launch_bounds__(GT) void gate_backward_kernel(GateBwdArgs a) {
     p = row_sum<LPT>(p);
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) g[i] = a.softmax ? s[i] * (g[i] - p) : g[i] * s[i] * (1.0f - s[i]);
+  for (int i = 0; i < V; ++i) g[i] = a.softmax ? s[i] * (g[i] - p) : g[i] * s[i];
   if (!here) return;
   if (vec) {
 #pragma unroll

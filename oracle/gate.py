@@ -72,5 +72,8 @@ def gate_backward(logits, score, renormalize, scale, idx, dw, ds=None):
             elif total > 0:
                 g[t, e] += (d - mean) / total
     if score == SIGMOID:
-        return g * s * (1.0 - s)
+        # s (1 - s): 1 - s itself has few bits where s is near 1
+        with np.errstate(invalid="ignore"):
+            z = np.exp(-np.abs(np.asarray(logits, np.float64)))
+        return g * z / (1.0 + z) ** 2
     return s * (g - (g * s).sum(axis=1, keepdims=True))

@@ -7,7 +7,7 @@ import torch
 import fp8_block_scaled_bias_amd as M
 from gpu_common import dev, host, log
 from oracle import gate as OG
-from test_gpu_gate import run_gate
+from test_gpu_gate import run_backward, run_gate
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +48,24 @@ def test_infinite_biases():
                                              max(1, n_group // 2), top, k, 1, 1.0)
                 assert (idx >= 0).all() and (idx < E).all() and (np.diff(idx, axis=1) > 0).all()
                 assert counts.sum() == 40 * k
+
+
+def test_sigmoid_gradient_of_saturated_scores():
+    """s (1 - s) where s is near 1 or near 0, to a few roundings of itself."""
+    E, k = 96, 4
+    l = np.concatenate([np.linspace(-86, 86, E), [0.0] * E, np.tile([10, -10, 20, -20, 40, -40], 16),
+                        np.linspace(12, 20, E)]).reshape(4, E).astype(np.float32)
+    rng = np.random.default_rng(1)
+    idx = np.stack([np.sort(rng.choice(E, k, replace=False)) for _ in range(4)])
+    dw, ds = rng.standard_normal((4, k)).astype(np.float32), rng.standard_normal((4, E)).astype(np.float32)
+    for given in (None, ds):
+        got = run_backward(dev(l), OG.SIGMOID, k, 0, 1.5, idx, dw, given)
+        ref = OG.gate_backward(l, OG.SIGMOID, 0, 1.5, idx, dw, given)
+        # the slope: exp 2, 1 + z, its reciprocal 1.5, both twice, two products:
+        # 9; then scale * dw 1 and the product 1, relative.  ds + scale * dw:
+        # one more, of the sum's parts, which may cancel
+        z = np.exp(-np.abs(l.astype(np.float64)))
+        part = np.zeros((4, E)) if given is None else np.abs(given).astype(np.float64)
+        for t in range(4):
+            part[t, idx[t]] += 1.5 * np.abs(dw[t])
+        assert (np.abs(got - ref) <= U * (11 * np.abs(ref) + 2 * part * z / (1 + z) ** 2) + 2.0 ** -149).all()
