@@ -9,6 +9,8 @@
 //   ds[e_j] += scale * dw_j                              (as they are)
 //   ds[e_j] += scale * (dw_j - sum_i dw_i s_i / S) / S   (renormalised)
 //   dl = s (ds - sum_e ds_e s_e)  (softmax),  ds s (1 - s)  (sigmoid)
+// (renormalised: with p_j = s_j / S, dl[e_j] += scale p_j (dw_j - sum_i dw_i p_i),
+// times 1 - s_j for a sigmoid).
 //
 // The order of the experts is that of the exact values: where the fp32 values
 // at the border between chosen and not chosen (of experts or of groups) are
@@ -337,6 +339,27 @@ __device__ __forceinline__ float sigmoid_slope(float l) {
 // exp(l - m), relative error (2.2 |l - m| + 2) roundings
 __device__ __forceinline__ float exp_from(float l, float m) {
   return __builtin_amdgcn_exp2f((l - m) * 1.4426950408889634f);
+}
+
+// s_j / sum_i s_i over the choices of a token, of which lane j of the row of 16
+// has the logit lj (-inf: none).  Scores relative to exp(c), c the largest
+// logit (for sigmoids at most 0): those of fp32 may all be 0 or subnormal.  0
+// where every logit is -inf.
+__device__ __forceinline__ float share(bool softmax, float lj) {
+  float c = row_max<16>(lj);
+  if (!softmax) c = fminf(c, 0.f);
+  if (c == -INFINITY) c = 0.f;
+  float e;
+  if (softmax) {
+    e = expf(lj - c);
+  } else {
+    const float z = expf(-fabsf(lj));
+    float up = lj >= 0.f ? 1.f : z;
+    if (c < 0.f) up = expf(lj - c);  // (no logit >= 0)
+    e = up / (1.0f + z);
+  }
+  const float sum = row_sum<16>(e);
+  return sum > 0.f ? e / sum : 0.f;
 }
 
 // LPT lanes hold a token, each 4 C of its logits: expert 4 (LPT c + lane) + j
@@ -786,37 +809,41 @@ __global__ __launch_bounds__(GT) void gate_backward_kernel(GateBwdArgs a) {
 #pragma unroll
     for (int i = 0; i < V; ++i) s[i] = sigmoid_slope(s[i]);
   }
-  // the choices' gradients (lanes 0..15 of a token; k <= 8)
+  // the choices' gradients (lanes 0..15 of a token; k <= 8).  Renormalised ones,
+  // p_j (dw_j - sum_i dw_i p_i) of the shares p, sum to 0 over a token, so they
+  // join behind the sum over the row; s_j (..) / S would overflow in 1 / S.
   float val = dwj;
   if (a.renorm) {
-    const float sj = id < 0 ? 0.f : a.softmax ? exp_from(lj, m) * inv : sigmoid_f32(lj);
-    const float S = row_sum<16>(sj);
-    const float r = S > 0.f ? 1.0f / S : 0.f;
-    const float mean = row_sum<16>(dwj * sj * r);
-    val = (dwj - mean) * r;
+    const float pj = share(a.softmax, id < 0 ? -INFINITY : lj);
+    val = pj * (dwj - row_sum<16>(dwj * pj));
+    if (!a.softmax) val *= sigmoid_f32(-lj);
   }
   float* buf = s_row[wv][sub];
+  auto add_choices = [&]() __attribute__((always_inline)) {  // to g
 #pragma unroll
-  for (int c = 0; c < C; ++c)
-    *reinterpret_cast<float4*>(buf + 4 * (LPT * c + l)) = make_float4(g[4 * c], g[4 * c + 1], g[4 * c + 2], g[4 * c + 3]);
-  if (l < k) {
-    s_id[wv][sub][l] = id;
-    s_val[wv][sub][l] = val;
-  }
-  __builtin_amdgcn_wave_barrier();
-  if (id >= 0) {
-    float sum = 0.f;
-    bool first = true;
-    for (int j = 0; j < k; ++j)
-      if (s_id[wv][sub][j] == id) {
-        first = first && j >= l;
-        sum += s_val[wv][sub][j];
-      }
-    if (first) buf[id] += sum;
-  }
-  __builtin_amdgcn_wave_barrier();
+    for (int c = 0; c < C; ++c)
+      *reinterpret_cast<float4*>(buf + 4 * (LPT * c + l)) =
+          make_float4(g[4 * c], g[4 * c + 1], g[4 * c + 2], g[4 * c + 3]);
+    if (l < k) {
+      s_id[wv][sub][l] = id;
+      s_val[wv][sub][l] = val;
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (id >= 0) {
+      float sum = 0.f;
+      bool first = true;
+      for (int j = 0; j < k; ++j)
+        if (s_id[wv][sub][j] == id) {
+          first = first && j >= l;
+          sum += s_val[wv][sub][j];
+        }
+      if (first) buf[id] += sum;
+    }
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-  for (int c = 0; c < C; ++c) load4(buf + 4 * (LPT * c + l), g + 4 * c);
+    for (int c = 0; c < C; ++c) load4(buf + 4 * (LPT * c + l), g + 4 * c);
+  };
+  if (!a.renorm) add_choices();
   float p = 0.f;
   if (a.softmax) {
 #pragma unroll
@@ -825,6 +852,7 @@ __global__ __launch_bounds__(GT) void gate_backward_kernel(GateBwdArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) g[i] = a.softmax ? s[i] * (g[i] - p) : g[i] * s[i];
+  if (a.renorm) add_choices();
   if (!here) return;
   if (vec) {
 #pragma unroll

@@ -59,21 +59,27 @@ def gate(logits, bias, score, n_group, topk_group, group_top, k, renormalize, sc
 
 
 def gate_backward(logits, score, renormalize, scale, idx, dw, ds=None):
-    s = gate_scores(logits, score)
+    l = np.asarray(logits, np.float64)
+    s = gate_scores(l, score)
     T, E = s.shape
+    # sigmoid: 1 - s and s (1 - s) from exp(-|l|), as 1 - s itself has few bits
+    # where s is near 1
+    with np.errstate(invalid="ignore"):
+        z = np.exp(-np.abs(l))
+    rest = np.where(l >= 0, z, 1.0) / (1.0 + z)
     g = np.zeros((T, E)) if ds is None else np.array(ds, np.float64)
+    extra = np.zeros((T, E))
     for t in range(T):
         named = [(int(e), scale * float(d)) for e, d in zip(idx[t], dw[t]) if 0 <= e < E]
         total = sum(s[t, e] for e, _ in named)
-        mean = sum(d * s[t, e] for e, d in named) / total if total > 0 else 0.0
+        mean = sum(d * (s[t, e] / total) for e, d in named) if total > 0 else 0.0
         for e, d in named:
             if not renormalize:
                 g[t, e] += d
             elif total > 0:
-                g[t, e] += (d - mean) / total
+                # ds_e (d - mean) / total, times s_e; its part of a softmax's
+                # sum over the row is 0
+                extra[t, e] += s[t, e] / total * (d - mean) * (1.0 if score == SOFTMAX else rest[t, e])
     if score == SIGMOID:
-        # s (1 - s): 1 - s itself has few bits where s is near 1
-        with np.errstate(invalid="ignore"):
-            z = np.exp(-np.abs(np.asarray(logits, np.float64)))
-        return g * z / (1.0 + z) ** 2
-    return s * (g - (g * s).sum(axis=1, keepdims=True))
+        return g * z / (1.0 + z) ** 2 + extra
+    return s * (g - (g * s).sum(axis=1, keepdims=True)) + extra

@@ -69,3 +69,58 @@ def test_sigmoid_gradient_of_saturated_scores():
         for t in range(4):
             part[t, idx[t]] += 1.5 * np.abs(dw[t])
         assert (np.abs(got - ref) <= U * (11 * np.abs(ref) + 2 * part * z / (1 + z) ** 2) + 2.0 ** -149).all()
+
+
+def low_choices(score, k, E=64):
+    """Rows whose k chosen logits lie far below zero (and below the row's
+    largest): their scores are subnormal or 0 in fp32.  Chosen: ids 3, 10, ..."""
+    rng = np.random.default_rng(k)
+    l = rng.standard_normal((7, E)).astype(np.float32)
+    chosen = 3 + 7 * np.arange(k)
+    for t, low in enumerate((-60.0, -86.0, -88.0, -95.0, -100.0, -104.0, -150.0)):
+        l[t, chosen] = low - np.arange(k) * 0.75
+    l[6, chosen[0]] = -80.0   # a spread of 70 between the choices
+    return l, np.tile(chosen, (7, 1))
+
+
+def share_bound(l, idx):
+    """Relative error of s_j / S: the logit's difference to the largest choice is
+    off by half a step, which exp turns into U * D; exp itself 2, 1 + z and its
+    quotient 2, three rounds of k - 1 additions at most 8, the last quotient 1."""
+    c = np.take_along_axis(l, idx, 1).astype(np.float64)
+    return ((c.max(axis=1) - c.min(axis=1))[:, None] + 13) * U
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("k", [1, 2, 8])
+@pytest.mark.parametrize("score", [OG.SOFTMAX, OG.SIGMOID])
+def test_renormalised_gradient_of_scores_below_fp32(score, k, kind):
+    l, idx = low_choices(score, k)
+    logits = dev(l) if kind == "f32" else dev(l).to(torch.bfloat16)
+    l = host(logits.float())
+    rng = np.random.default_rng(2)
+    dw = rng.standard_normal((7, k)).astype(np.float32)
+    ds = rng.standard_normal((7, l.shape[1])).astype(np.float32)
+    for given in (None, ds):
+        got = run_backward(logits, score, k, 1, 1.5, idx, dw, given)
+        ref = OG.gate_backward(l, score, 1, 1.5, idx, dw, given)
+        assert np.isfinite(got).all()
+        # p_j (dw_j - mean): the shares' errors in it and in the mean, and five
+        # roundings (scale * dw, the product and sum of the mean, difference,
+        # product), times 1 - s_j (6 roundings)
+        p = np.exp(np.take_along_axis(l, idx, 1).astype(np.float64))
+        p /= p.sum(axis=1, keepdims=True)     # all far below 0: s = exp(l)
+        a = 1.5 * np.abs(dw)
+        part = np.zeros(l.shape)
+        np.put_along_axis(part, idx, p * (a + (a * p).sum(axis=1, keepdims=True)), axis=1)
+        tol = (3 * share_bound(l, idx) + 14 * U) * part + 2.0 ** -149
+        if given is not None:
+            # s (ds - sum ds s) of logits within 5 of the largest or under
+            # e^-60: 2 |l - m| + 2 roundings of exp, 10 of the sum, quotient
+            s = OG.gate_scores(l, score)
+            size = s * (np.abs(ds) + (s * np.abs(ds)).sum(axis=1, keepdims=True))
+            tol = tol + 80 * U * size + 2.0 ** -125
+        if kind == "bf16":
+            tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref) + 2.0 ** -134
+        bad = np.argwhere(np.abs(got - ref) > tol)
+        assert bad.size == 0, (bad[:5].tolist(), got[tuple(bad[0])], ref[tuple(bad[0])], tol[tuple(bad[0])])
