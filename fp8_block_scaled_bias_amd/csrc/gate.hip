@@ -122,16 +122,89 @@ __device__ __forceinline__ float wave_max(float v) {
   return over_row<64>([](float a, float b) { return fmaxf(a, b); }, v);
 }
 
+// whole numbers in the order of the floats (and back): their maxima need no
+// care for NaN, which would cost an instruction each
+__device__ __forceinline__ int order_key(float x) {
+  const int b = __float_as_int(x);
+  return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float from_key(int b) { return __int_as_float(b ^ ((b >> 31) & 0x7FFFFFFF)); }
+
+// 1 / (1 + exp(-l)) with a relative error of 6 roundings at any l
+__device__ __forceinline__ float sigmoid_f32(float l) {
+  const float z = expf(-fabsf(l)), d = 1.0f + z;  // d in [1, 2]
+  float y = __builtin_amdgcn_rcpf(d);
+  y = fmaf(fmaf(-d, y, 1.0f), y, y);
+  return l >= 0.f ? y : z * y;
+}
+// its slope, s (1 - s) = z / (1 + z)^2 with z = exp(-|l|): 1 - s of a rounded s
+// has no bits left where s is near 1.  Relative error 9 roundings at any l.
+__device__ __forceinline__ float sigmoid_slope(float l) {
+  const float z = expf(-fabsf(l)), d = 1.0f + z;
+  float y = __builtin_amdgcn_rcpf(d);
+  y = fmaf(fmaf(-d, y, 1.0f), y, y);
+  return z * y * y;
+}
+// exp(l - m), relative error (2.2 |l - m| + 2) roundings
+__device__ __forceinline__ float exp_from(float l, float m) {
+  return __builtin_amdgcn_exp2f((l - m) * 1.4426950408889634f);
+}
+
+// s_j / sum_i s_i over the choices of a token, of which lane j of the row of 16
+// has the logit lj (-inf: none); m, inv: the softmax's largest logit and 1 /
+// sum.  Scores relative to exp(c), c the largest logit (for sigmoids at most 0):
+// those of fp32 may be subnormal.  0 where they are all 0.
+__device__ __forceinline__ float share(bool softmax, float lj, float m, float inv) {
+  const float c = row_max<16>(lj);
+  float e;
+  bool some = true;
+  if (softmax) {
+    some = exp_from(c, m) * inv > 0.f;
+    e = expf(lj - c);
+  } else {
+    const float z = expf(-fabsf(lj));
+    float up = lj >= 0.f ? 1.f : z;
+    if (c < 0.f) {  // (no logit >= 0)
+      some = sigmoid_f32(c) > 0.f;
+      up = expf(lj - c);
+    }
+    e = up / (1.0f + z);
+  }
+  const float sum = row_sum<16>(e);
+  return some ? e / sum : 0.f;
+}
+
+// Ids and weights of token t by the first 16 lanes of its row (l), whose choices
+// stand in ids in any order; m, inv: the softmax's largest logit and 1 / sum.
+template <typename D, bool ONE>
+__device__ __forceinline__ void write_choice(const GateArgs& a, int64_t t, const D* row, const int* ids,
+                                             int l, float m, float inv, int* s_hist) {
+  const int k = a.k;
+  int id = 0, place = 0;
+  float lj = -INFINITY;
+  if (l < k) {
+    id = ids[l];
+    for (int j = 0; j < k; ++j) place += ids[j] < id ? 1 : 0;
+    lj = load_logit(row + id);
+  }
+  const float w = a.renorm ? share(a.softmax, lj, m, inv) : a.softmax ? exp_from(lj, m) * inv : sigmoid_f32(lj);
+  if (l < k) {
+    a.topk_idx[t * k + place] = id;
+    a.topk_w[t * k + place] = a.scale * w;
+    if (ONE) atomicAdd(&s_hist[id], 1);
+  }
+}
+
 // One token by one wave, its order in 64 bits; expert i * 64 + lane sits in
 // slot i of a lane.  s_v: the wave's [64 VPL] doubles, s_g: its [GMAXG].  The
 // code is small (one exp in a rolled loop): it is read cold.
 template <typename D, int VPL, bool ONE>
 __device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double* s_v, double* s_g,
-                                           int* s_hist) {
+                                           int* s_ids, int* s_hist) {
   const int lane = threadIdx.x & 63;
   const D* row = static_cast<const D*>(a.logits) + t * a.E;
   const int E = a.E, size = a.size;
-  float l[VPL], s[VPL], bias[VPL];
+  float l[VPL], bias[VPL];
   double v[VPL];
   float m = -INFINITY;
 #pragma unroll
@@ -158,7 +231,6 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double*
   for (int i = 0; i < VPL; ++i) {
     const double y = s_v[i * 64 + lane];
     v[i] = a.softmax ? y * inv : (l[i] >= 0.f ? 1.0 : y) / (1.0 + y);
-    s[i] = (float)v[i];
   }
   // values of the order; excluded experts (-inf or NaN) below every other,
   // slots that are no candidates at -inf
@@ -239,35 +311,19 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double*
     meet(partner<5>(best), partner<5>(at));
     if ((at & 63) == lane) taken |= 1u << (at >> 6);
   }
-  // ids ascending: slots in order, lanes in order within a slot
   const uint64_t below = (1ull << lane) - 1ull;
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) sum += ((taken >> i) & 1) ? s[i] : 0.f;
-  sum = wave_sum(sum);
   int base = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const bool mine = (taken >> i) & 1;
     const uint64_t msk = __ballot(mine);
-    if (mine) {
-      const int64_t o = t * a.k + base + __popcll(msk & below);
-      a.topk_idx[o] = i * 64 + lane;
-      const float w = a.renorm ? (sum > 0.f ? s[i] / sum : 0.f) : s[i];
-      a.topk_w[o] = w * a.scale;
-      if (ONE) atomicAdd(&s_hist[i * 64 + lane], 1);
-    }
+    if (mine) s_ids[base + __popcll(msk & below)] = i * 64 + lane;
     base += __popcll(msk);
   }
+  __builtin_amdgcn_wave_barrier();
+  if (lane < 16)
+    write_choice<D, ONE>(a, t, row, s_ids, lane, m > -INFINITY ? m : 0.f, (float)inv, s_hist);
 }
-
-// whole numbers in the order of the floats (and back): their maxima need no
-// care for NaN, which would cost an instruction each
-__device__ __forceinline__ int order_key(float x) {
-  const int b = __float_as_int(x);
-  return b ^ ((b >> 31) & 0x7FFFFFFF);
-}
-__device__ __forceinline__ float from_key(int b) { return __int_as_float(b ^ ((b >> 31) & 0x7FFFFFFF)); }
 
 __device__ __forceinline__ void order2(int& hi, int& lo) {
   const int a = max(hi, lo), b = min(hi, lo);
@@ -319,47 +375,6 @@ __device__ __forceinline__ int row_scan(int v, int l) {
     v += (l >= 16 ? r0 : 0) + (l >= 32 ? r1 : 0) + (l >= 48 ? r2 : 0);
   }
   return v;
-}
-
-// 1 / (1 + exp(-l)) with a relative error of 6 roundings at any l
-__device__ __forceinline__ float sigmoid_f32(float l) {
-  const float z = expf(-fabsf(l)), d = 1.0f + z;  // d in [1, 2]
-  float y = __builtin_amdgcn_rcpf(d);
-  y = fmaf(fmaf(-d, y, 1.0f), y, y);
-  return l >= 0.f ? y : z * y;
-}
-// its slope, s (1 - s) = z / (1 + z)^2 with z = exp(-|l|): 1 - s of a rounded s
-// has no bits left where s is near 1.  Relative error 9 roundings at any l.
-__device__ __forceinline__ float sigmoid_slope(float l) {
-  const float z = expf(-fabsf(l)), d = 1.0f + z;
-  float y = __builtin_amdgcn_rcpf(d);
-  y = fmaf(fmaf(-d, y, 1.0f), y, y);
-  return z * y * y;
-}
-// exp(l - m), relative error (2.2 |l - m| + 2) roundings
-__device__ __forceinline__ float exp_from(float l, float m) {
-  return __builtin_amdgcn_exp2f((l - m) * 1.4426950408889634f);
-}
-
-// s_j / sum_i s_i over the choices of a token, of which lane j of the row of 16
-// has the logit lj (-inf: none).  Scores relative to exp(c), c the largest
-// logit (for sigmoids at most 0): those of fp32 may all be 0 or subnormal.  0
-// where every logit is -inf.
-__device__ __forceinline__ float share(bool softmax, float lj) {
-  float c = row_max<16>(lj);
-  if (!softmax) c = fminf(c, 0.f);
-  if (c == -INFINITY) c = 0.f;
-  float e;
-  if (softmax) {
-    e = expf(lj - c);
-  } else {
-    const float z = expf(-fabsf(lj));
-    float up = lj >= 0.f ? 1.f : z;
-    if (c < 0.f) up = expf(lj - c);  // (no logit >= 0)
-    e = up / (1.0f + z);
-  }
-  const float sum = row_sum<16>(e);
-  return sum > 0.f ? e / sum : 0.f;
 }
 
 // LPT lanes hold a token, each 4 C of its logits: expert 4 (LPT c + lane) + j
@@ -639,20 +654,7 @@ __global__ __launch_bounds__(GT) void gate_kernel(GateArgs a) {
     }
     __builtin_amdgcn_wave_barrier();
     if (clean && l < 16) {
-      float sj = 0.f;
-      int id = 0, place = 0;
-      if (l < k) {
-        id = s_ids[wv][sub][l];
-        for (int j = 0; j < k; ++j) place += s_ids[wv][sub][j] < id ? 1 : 0;
-        const float lj = load_logit(row + id);
-        sj = a.softmax ? exp_from(lj, m) * inv : sigmoid_f32(lj);
-      }
-      const float sum = row_sum<16>(sj);
-      if (l < k) {
-        a.topk_idx[t * k + place] = id;
-        a.topk_w[t * k + place] = a.scale * (a.renorm ? (sum > 0.f ? sj / sum : 0.f) : sj);
-        if (ONE) atomicAdd(&s_hist[id], 1);
-      }
+      write_choice<D, ONE>(a, t, row, s_ids[wv][sub], l, m, inv, s_hist);
     } else if (here && l == 0) {
       a.topk_idx[t * k] = -1;  // for the second look
     }
@@ -664,7 +666,7 @@ __global__ __launch_bounds__(GT) void gate_kernel(GateArgs a) {
       uint64_t todo = __ballot(in && ((volatile int32_t*)a.topk_idx)[(in ? t0 + lane : 0) * k] == -1);
       for (; todo; todo &= todo - 1)
         gate_token<D, EMAX / 64, ONE>(a, t0 + __ffsll((unsigned long long)todo) - 1,
-                                      reinterpret_cast<double*>(s_mem[wv]), s_g[wv], s_hist);
+                                      reinterpret_cast<double*>(s_mem[wv]), s_g[wv], s_ids[wv][0], s_hist);
     }
   }
   if (ONE) {
@@ -814,7 +816,7 @@ __global__ __launch_bounds__(GT) void gate_backward_kernel(GateBwdArgs a) {
   // join behind the sum over the row; s_j (..) / S would overflow in 1 / S.
   float val = dwj;
   if (a.renorm) {
-    const float pj = share(a.softmax, id < 0 ? -INFINITY : lj);
+    const float pj = share(a.softmax, id < 0 ? -INFINITY : lj, m, inv);
     val = pj * (dwj - row_sum<16>(dwj * pj));
     if (!a.softmax) val *= sigmoid_f32(-lj);
   }

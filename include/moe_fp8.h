@@ -621,7 +621,8 @@ int moe_router_logits_backward(const void* x_bf16, const float* centroids, const
  *   are kept (n_group 1: every expert is); the k largest v among the kept
  *   experts are chosen; ties go to the lower index; ids are written in
  *   ascending order;
- *   w[j] = scale * s[e_j] / sum_j' s[e_j']  (renormalize 1; 0 if the sum is 0)
+ *   w[j] = scale * s[e_j] / sum_j' s[e_j']  (renormalize 1; 0 if every s[e_j] is
+ *                                           0 in fp32)
  *          scale * s[e_j]                   (renormalize 0)
  *   expert_counts[e] = number of tokens that chose e (overwritten).
  * The choice is that of the exact s and v of the given logits and bias: where
@@ -630,6 +631,7 @@ int moe_router_logits_backward(const void* x_bf16, const float* centroids, const
  * where fewer than k others are kept, a row of nothing but -inf has weights 0;
  * so does a bias of -inf, which leaves the score as it is.  Logits of +inf or
  * NaN give unspecified scores and weights, and k different ids in [0, E).
+ * A softmax score under 2^-126, a sigmoid's under 2^-149, may be 0 in fp32.
  *
  * logits          [T, E] fp32 (logits_type MOE_TYPE_F32) or bf16 (MOE_TYPE_BF16)
  * bias            [E] fp32, or NULL
@@ -652,7 +654,7 @@ int moe_gate(const void* logits, int32_t logits_type, int64_t T, int32_t E, cons
  *   ds[e]  = d_scores[t, e] (0 if NULL), and for every chosen e_j
  *     renormalize 0:  ds[e_j] += scale * dw_j
  *     renormalize 1:  ds[e_j] += scale * (dw_j - sum_i dw_i s_i / S) / S,
- *                     S = sum_i s[e_i]  (nothing if S is 0)
+ *                     S = sum_i s[e_i]  (nothing if every s[e_i] is 0 in fp32)
  *   d_logits[t, e] = s[e] * (ds[e] - sum_i ds[i] s[i])   (softmax)
  *                    ds[e] * s[e] * (1 - s[e])            (sigmoid)
  * logits, score, renormalize, scale as in moe_gate; topk_idx [T, k] its choice

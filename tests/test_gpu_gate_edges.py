@@ -71,16 +71,26 @@ def test_sigmoid_gradient_of_saturated_scores():
         assert (np.abs(got - ref) <= U * (11 * np.abs(ref) + 2 * part * z / (1 + z) ** 2) + 2.0 ** -149).all()
 
 
+LOWS = (-60.0, -86.0, -88.0, -95.0, -100.0, -110.0, -150.0)
+
+
 def low_choices(score, k, E=64):
     """Rows whose k chosen logits lie far below zero (and below the row's
     largest): their scores are subnormal or 0 in fp32.  Chosen: ids 3, 10, ..."""
     rng = np.random.default_rng(k)
     l = rng.standard_normal((7, E)).astype(np.float32)
     chosen = 3 + 7 * np.arange(k)
-    for t, low in enumerate((-60.0, -86.0, -88.0, -95.0, -100.0, -104.0, -150.0)):
+    for t, low in enumerate(LOWS):
         l[t, chosen] = low - np.arange(k) * 0.75
-    l[6, chosen[0]] = -80.0   # a spread of 70 between the choices
+    l[1, chosen[0]] = -60.0   # a spread of 26 to 31 between the choices
     return l, np.tile(chosen, (7, 1))
+
+
+def nothing(l, idx, score):
+    """Rows whose chosen scores have to count as 0 in fp32, and those where they
+    may: under half of 2^-149 and, for a softmax, under 2^-126."""
+    most = np.take_along_axis(OG.gate_scores(l, score), idx, 1).max(axis=1)
+    return most < 0.99 * 2.0 ** -150, most < (1.01 * 2.0 ** -126 if score == OG.SOFTMAX else 2.0 ** -148)
 
 
 def share_bound(l, idx):
@@ -122,5 +132,36 @@ def test_renormalised_gradient_of_scores_below_fp32(score, k, kind):
             tol = tol + 80 * U * size + 2.0 ** -125
         if kind == "bf16":
             tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref) + 2.0 ** -134
-        bad = np.argwhere(np.abs(got - ref) > tol)
-        assert bad.size == 0, (bad[:5].tolist(), got[tuple(bad[0])], ref[tuple(bad[0])], tol[tuple(bad[0])])
+        # without the choices' part
+        rest = ref - OG.gate_backward(l, score, 1, 1.5, idx, dw, None)
+        must, may = nothing(l, idx, score)
+        ok = (np.abs(got - ref) <= tol).all(axis=1)
+        empty = (np.abs(got - rest) <= tol).all(axis=1)
+        assert np.where(must, empty, ok | (may & empty)).all(), (ok, empty, must, may)
+
+
+@pytest.mark.parametrize("k", [1, 2, 8])
+@pytest.mark.parametrize("score", [OG.SOFTMAX, OG.SIGMOID])
+@pytest.mark.parametrize("tie", [False, True])
+def test_renormalised_weights_of_scores_below_fp32(score, k, tie):
+    """A bias chooses experts whose scores are subnormal or 0 in fp32: the weights
+    are still their shares.  tie: one more expert ties at the border, so that the
+    order is looked at in 64 bits."""
+    l, idx = low_choices(score, k)
+    bias = np.zeros(l.shape[1], np.float32)
+    bias[idx[0]] = 4.0
+    if tie:
+        bias[-1] = 4.0
+        l[:, -1] = -170.0
+    args = (score, 1, 1, 1, k, 1, 1.5)
+    ref = OG.gate(l, bias, *args)
+    assert np.array_equal(ref["idx"], idx)
+    got, w, counts, _ = run_gate(dev(l), bias, *args)
+    assert np.array_equal(got, idx) and np.array_equal(counts, ref["counts"])
+    must, may = nothing(l, idx, score)
+    ok = (np.abs(w - ref["w"]) <= (share_bound(l, idx) + 2 * U) * ref["w"] + 2.0 ** -149).all(axis=1)
+    empty = (w == 0).all(axis=1)
+    assert np.where(must, empty, ok | (may & empty)).all(), (ok, empty, must, may)
+    # every logit -inf: weights 0
+    _, w, _, _ = run_gate(dev(np.full_like(l, -np.inf)), bias, *args)
+    assert (w == 0).all()
