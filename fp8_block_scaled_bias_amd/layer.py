@@ -91,7 +91,9 @@ class Gate:
     """A router in one of moe_gate's forms: score SCORE_SOFTMAX or
     SCORE_SIGMOID; use_bias: the layer's bias moves the choice; groups (of the
     shape) by their group_top largest; renormalize: a token's weights sum to
-    scale, else they are scale times the scores."""
+    scale, else they are scale times the scores.  The layer's backward needs a
+    number of experts that is a multiple of 16; its sequence-wise balance term
+    (seq_len) goes with moe_route only."""
     score: int = L.SCORE_SOFTMAX
     use_bias: bool = True
     group_top: int = 2
@@ -308,6 +310,7 @@ class MoELayer:
         side stream (default priority) that forks from the launch stream
         before the router and joins it before the first expert GEMM, so the
         two overlap."""
+        self._check_gate(seq_len)
         s = self.shape
         T = x_bf16.shape[0]
         b = bufs or self.buffers(T)
@@ -407,6 +410,9 @@ class MoELayer:
         `events` as in forward, keys "combine_bwd", "dgrad_down",
         "recompute_gate_up", "swiglu_bwd", "dgrad_gate_up", "unpermute",
         "wgrad_down", "wgrad_gate_up", "router_bwd"."""
+        self._check_gate(seq_len)
+        if self.gate is not None and self.shape.E % 16:
+            raise ValueError(f"the backward of a layer with a Gate needs E % 16 == 0, E is {self.shape.E}")
         s = self.shape
         T = dy_bf16.shape[0]
         b = bufs or self.buffers(T)
@@ -462,8 +468,6 @@ class MoELayer:
             L.grouped_fp8_wgrad(bb.c_dgu, bb.s_dgu, bb.c_x, bb.s_x, cap, b.offsets, G, R, 2 * I, H,
                                 bb.dW_gu, st)))
         if self.gate is not None:
-            if seq_len is not None:
-                raise ValueError("the sequence-wise balance term needs moe_route's scores: no Gate")
             g = self.gate
             bb.dense()
             step("router_bwd", lambda: (
@@ -489,12 +493,15 @@ class MoELayer:
                 bb.dense_ws_bytes, st))
         return bb
 
+    def _check_gate(self, seq_len):
+        """What a layer with a Gate does not do, before anything is launched."""
+        if self.gate is not None and seq_len is not None:
+            raise ValueError("the sequence-wise balance term needs moe_route's scores: no Gate")
+
     def _route(self, x_bf16, b, seq_len, stream):
         s = self.shape
         T = x_bf16.shape[0]
         if self.gate is not None:
-            if seq_len is not None:
-                raise ValueError("the sequence-wise balance term needs moe_route's scores: no Gate")
             g = self.gate
             L.moe_router_logits(x_bf16, T, s.H, self.centroids, s.E, b.logits, b.route_ws,
                                 b.route_ws_bytes, stream)
