@@ -116,8 +116,6 @@ class Buffers:
         self.counts = torch.empty((s.E,), dtype=i32, device=dev)
         self.route_ws_bytes = max(16, L.moe_route_workspace_bytes(T, s.H, s.E))
         self.route_ws = torch.empty((self.route_ws_bytes,), dtype=u8, device=dev)
-        self.xq = torch.empty((T, s.H), dtype=u8, device=dev)
-        self.xs = torch.empty((T, s.H // 128), dtype=f32, device=dev)
         self.offsets = torch.empty((s.G + 1,), dtype=i32, device=dev)
         self.perm_src = torch.empty((max(R, 1),), dtype=i32, device=dev)
         self.inv_perm = torch.empty((max(T * s.k, 1),), dtype=i32, device=dev)
@@ -127,10 +125,18 @@ class Buffers:
         self._logits = None
         self._dev = dev
         self._shape = s
-        self.hq = torch.empty((R, s.I), dtype=u8, device=dev)
-        self.hs = torch.empty((R, s.I // 128), dtype=f32, device=dev)
         self.d = torch.empty((R, s.H), dtype=bf, device=dev)
         self.y = torch.empty((T, s.H), dtype=bf, device=dev)
+        self._operands()
+
+    def _operands(self):
+        """The expert products' operands: x and h in E4M3 with 1x128 scales."""
+        s, T, R, dev = self._shape, self.T, self.R, self._dev
+        u8, f32 = torch.uint8, torch.float32
+        self.xq = torch.empty((T, s.H), dtype=u8, device=dev)
+        self.xs = torch.empty((T, s.H // 128), dtype=f32, device=dev)
+        self.hq = torch.empty((R, s.I), dtype=u8, device=dev)
+        self.hs = torch.empty((R, s.I // 128), dtype=f32, device=dev)
 
     def balance(self, seq_len: int):
         """Buffers of the sequence-wise balance statistic (allocated on first
@@ -527,9 +533,9 @@ class MoELayer:
 class Int8Buffers(Buffers):
     """Device buffers of one int8 forward at T tokens (reused across calls)."""
 
-    def __init__(self, shape: LayerShape, T: int, device="cuda"):
-        super().__init__(shape, T, device)
-        s, R, dev = shape, self.R, self._dev
+    def _operands(self):
+        """x in 8-bit integers with a scale for each token; h in bf16, then as x."""
+        s, T, R, dev = self._shape, self.T, self.R, self._dev
         i8, f32 = torch.int8, torch.float32
         self.xq = torch.empty((T, s.H), dtype=i8, device=dev)
         self.xs = torch.empty((T,), dtype=f32, device=dev)
