@@ -895,7 +895,19 @@ void launch_gate(const GateArgs& a, hipStream_t st) {
 
 template <typename D, int LPT, int C>
 void launch_backward_as(const GateBwdArgs& a, hipStream_t st) {
-  gate_backward_kernel<D, LPT, C><<<dim3((unsigned)ceil_div(a.T, GT / LPT)), dim3(GT), 0, st>>>(a);
+  // a launch holds less than 2^32 threads: runs of 2^25 tokens (offsets that
+  // keep every tensor's alignment)
+  constexpr int64_t RUN = 1ll << 25;
+  for (int64_t t = 0; t < a.T; t += RUN) {
+    GateBwdArgs r = a;
+    r.T = std::min(RUN, a.T - t);
+    r.logits = static_cast<const D*>(a.logits) + t * a.E;
+    r.idx += t * a.k;
+    r.dw += t * a.k;
+    if (a.ds) r.ds += t * a.E;
+    r.dl = static_cast<D*>(a.dl) + t * a.E;
+    gate_backward_kernel<D, LPT, C><<<dim3((unsigned)ceil_div(r.T, GT / LPT)), dim3(GT), 0, st>>>(r);
+  }
 }
 
 template <typename D>

@@ -165,3 +165,34 @@ def test_renormalised_weights_of_scores_below_fp32(score, k, tie):
     # every logit -inf: weights 0
     _, w, _, _ = run_gate(dev(np.full_like(l, -np.inf)), bias, *args)
     assert (w == 0).all()
+
+
+def test_more_tokens_than_one_launch_holds():
+    """Two experts, 2^28 + 77 tokens: sixteen threads a token are more than 2^32."""
+    T, E = (1 << 28) + 77, 2
+    log(f"[gate] T={T}")
+    logits = torch.empty((T, E), dtype=torch.bfloat16, device="cuda")
+    logits.normal_(generator=torch.Generator(device="cuda").manual_seed(3))
+    idx = torch.full((T, 1), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T, 1), np.nan, device="cuda")
+    counts = torch.empty(E, dtype=torch.int32, device="cuda")
+    M.moe_gate(logits, T, E, None, OG.SOFTMAX, 1, 1, 1, 1, 0, 1.0, idx, w, counts)
+    dl = torch.full((T, E), np.nan, dtype=torch.bfloat16, device="cuda")
+    M.moe_gate_backward(logits, T, E, OG.SOFTMAX, 1, 0, 1.0, idx, w, dl)
+    torch.cuda.synchronize()
+    assert int(counts.sum()) == T
+    first = (logits[:, :1] >= logits[:, 1:]).to(torch.int32)   # a tie goes to the lower index
+    assert torch.equal(idx, 1 - first)
+    del first
+    rows = np.unique(np.concatenate([np.arange(0, T, T // 997), np.arange(2 ** 25 - 3, 2 ** 25 + 3),
+                                     np.arange(2 ** 28 - 3, 2 ** 28 + 3), np.arange(T - 40, T)]))
+    at = torch.from_numpy(rows).cuda()
+    l = host(logits[at].float())
+    ref = OG.gate(l, None, OG.SOFTMAX, 1, 1, 1, 1, 0, 1.0)
+    assert np.array_equal(host(idx[at]), ref["idx"])
+    # exp, sum, quotient, product of logits within 12 of each other
+    assert (np.abs(host(w[at]) - ref["w"]) <= 40 * U * ref["w"]).all()
+    want = OG.gate_backward(l, OG.SOFTMAX, 0, 1.0, ref["idx"], host(w[at]))
+    # w s (1 - s): w off by its bound, the difference by the parts' roundings
+    assert (np.abs(host(dl[at].float()) - want) <= 2.0 ** -8 * np.abs(want) + 200 * U).all()
+    assert bool(torch.isfinite(dl).all())
