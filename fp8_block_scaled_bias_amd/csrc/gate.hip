@@ -150,49 +150,23 @@ __device__ __forceinline__ float exp_from(float l, float m) {
   return __builtin_amdgcn_exp2f((l - m) * 1.4426950408889634f);
 }
 
-// s_j / sum_i s_i over the choices of a token, of which lane j of the row of 16
-// has the logit lj (-inf: none); m, inv: the softmax's largest logit and 1 /
-// sum.  Scores relative to exp(c), c the largest logit (for sigmoids at most 0):
-// those of fp32 may be subnormal.  0 where they are all 0.
-__device__ __forceinline__ float share(bool softmax, float lj, float m, float inv) {
-  const float c = row_max<16>(lj);
-  float e;
-  bool some = true;
-  if (softmax) {
-    some = exp_from(c, m) * inv > 0.f;
-    e = expf(lj - c);
-  } else {
-    const float z = expf(-fabsf(lj));
-    float up = lj >= 0.f ? 1.f : z;
-    if (c < 0.f) {  // (no logit >= 0)
-      some = sigmoid_f32(c) > 0.f;
-      up = expf(lj - c);
-    }
-    e = up / (1.0f + z);
-  }
-  const float sum = row_sum<16>(e);
-  return some ? e / sum : 0.f;
-}
+// Under such a sum S of chosen scores those under 2^-126 (0 in a softmax, or
+// subnormal) would be more than 2^-62 of it.  The scores are exp(l) times one
+// factor there (1 + exp(l) is 1), so that s_j / S can be formed of exp(l_j - c),
+// c the largest logit chosen.
+constexpr float kLow = 0x1p-64f;
 
-// Ids and weights of token t by the first 16 lanes of its row (l), whose choices
-// stand in ids in any order; m, inv: the softmax's largest logit and 1 / sum.
-template <typename D, bool ONE>
-__device__ __forceinline__ void write_choice(const GateArgs& a, int64_t t, const D* row, const int* ids,
-                                             int l, float m, float inv, int* s_hist) {
-  const int k = a.k;
-  int id = 0, place = 0;
-  float lj = -INFINITY;
-  if (l < k) {
-    id = ids[l];
-    for (int j = 0; j < k; ++j) place += ids[j] < id ? 1 : 0;
-    lj = load_logit(row + id);
+// s_j / S over the choices of a token, of which lane j of the row of 16 has the
+// logit lj (-inf: none); m, inv: the softmax's largest logit and 1 / sum.  0
+// where all scores are 0 in fp32.
+__device__ __forceinline__ float share(bool softmax, float lj, float m, float inv) {
+  float s = softmax ? exp_from(lj, m) * inv : sigmoid_f32(lj);
+  float sum = row_sum<16>(s);
+  if (sum > 0.f && sum < kLow) {
+    s = exp_from(lj, row_max<16>(lj));
+    sum = row_sum<16>(s);
   }
-  const float w = a.renorm ? share(a.softmax, lj, m, inv) : a.softmax ? exp_from(lj, m) * inv : sigmoid_f32(lj);
-  if (l < k) {
-    a.topk_idx[t * k + place] = id;
-    a.topk_w[t * k + place] = a.scale * w;
-    if (ONE) atomicAdd(&s_hist[id], 1);
-  }
+  return sum > 0.f ? s / sum : 0.f;
 }
 
 // One token by one wave, its order in 64 bits; expert i * 64 + lane sits in
@@ -200,11 +174,11 @@ __device__ __forceinline__ void write_choice(const GateArgs& a, int64_t t, const
 // code is small (one exp in a rolled loop): it is read cold.
 template <typename D, int VPL, bool ONE>
 __device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double* s_v, double* s_g,
-                                           int* s_ids, int* s_hist) {
+                                           int* s_hist) {
   const int lane = threadIdx.x & 63;
   const D* row = static_cast<const D*>(a.logits) + t * a.E;
   const int E = a.E, size = a.size;
-  float l[VPL], bias[VPL];
+  float l[VPL], s[VPL], bias[VPL];
   double v[VPL];
   float m = -INFINITY;
 #pragma unroll
@@ -231,6 +205,7 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double*
   for (int i = 0; i < VPL; ++i) {
     const double y = s_v[i * 64 + lane];
     v[i] = a.softmax ? y * inv : (l[i] >= 0.f ? 1.0 : y) / (1.0 + y);
+    s[i] = (float)v[i];
   }
   // values of the order; excluded experts (-inf or NaN) below every other,
   // slots that are no candidates at -inf
@@ -311,18 +286,39 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double*
     meet(partner<5>(best), partner<5>(at));
     if ((at & 63) == lane) taken |= 1u << (at >> 6);
   }
+  // ids ascending: slots in order, lanes in order within a slot
   const uint64_t below = (1ull << lane) - 1ull;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) sum += ((taken >> i) & 1) ? s[i] : 0.f;
+  sum = wave_sum(sum);
+  if (a.renorm && sum > 0.f && sum < kLow) {  // (as in share)
+    float c = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) c = ((taken >> i) & 1) ? fmaxf(c, l[i]) : c;
+    c = wave_max(c);
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      s[i] = exp_from(l[i], c);
+      sum += ((taken >> i) & 1) ? s[i] : 0.f;
+    }
+    sum = wave_sum(sum);
+  }
   int base = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const bool mine = (taken >> i) & 1;
     const uint64_t msk = __ballot(mine);
-    if (mine) s_ids[base + __popcll(msk & below)] = i * 64 + lane;
+    if (mine) {
+      const int64_t o = t * a.k + base + __popcll(msk & below);
+      a.topk_idx[o] = i * 64 + lane;
+      const float w = a.renorm ? (sum > 0.f ? s[i] / sum : 0.f) : s[i];
+      a.topk_w[o] = w * a.scale;
+      if (ONE) atomicAdd(&s_hist[i * 64 + lane], 1);
+    }
     base += __popcll(msk);
   }
-  __builtin_amdgcn_wave_barrier();
-  if (lane < 16)
-    write_choice<D, ONE>(a, t, row, s_ids, lane, m > -INFINITY ? m : 0.f, (float)inv, s_hist);
 }
 
 __device__ __forceinline__ void order2(int& hi, int& lo) {
@@ -653,11 +649,27 @@ __global__ __launch_bounds__(GT) void gate_kernel(GateArgs a) {
       }
     }
     __builtin_amdgcn_wave_barrier();
+    bool low = false;  // the scores' sum: for the second look
     if (clean && l < 16) {
-      write_choice<D, ONE>(a, t, row, s_ids[wv][sub], l, m, inv, s_hist);
+      float sj = 0.f;
+      int id = 0, place = 0;
+      if (l < k) {
+        id = s_ids[wv][sub][l];
+        for (int j = 0; j < k; ++j) place += s_ids[wv][sub][j] < id ? 1 : 0;
+        const float lj = load_logit(row + id);
+        sj = a.softmax ? exp_from(lj, m) * inv : sigmoid_f32(lj);
+      }
+      const float sum = row_sum<16>(sj);
+      low = a.renorm && sum > 0.f && sum < kLow;
+      if (l < k) {
+        a.topk_idx[t * k + place] = low && place == 0 ? -1 : id;
+        a.topk_w[t * k + place] = a.scale * (a.renorm ? (sum > 0.f ? sj / sum : 0.f) : sj);
+        if (ONE && !low) atomicAdd(&s_hist[id], 1);
+      }
     } else if (here && l == 0) {
       a.topk_idx[t * k] = -1;  // for the second look
     }
+    any |= __ballot(low);
     __builtin_amdgcn_wave_barrier();
   }
   if (any) {
@@ -666,7 +678,7 @@ __global__ __launch_bounds__(GT) void gate_kernel(GateArgs a) {
       uint64_t todo = __ballot(in && ((volatile int32_t*)a.topk_idx)[(in ? t0 + lane : 0) * k] == -1);
       for (; todo; todo &= todo - 1)
         gate_token<D, EMAX / 64, ONE>(a, t0 + __ffsll((unsigned long long)todo) - 1,
-                                      reinterpret_cast<double*>(s_mem[wv]), s_g[wv], s_ids[wv][0], s_hist);
+                                      reinterpret_cast<double*>(s_mem[wv]), s_g[wv], s_hist);
     }
   }
   if (ONE) {

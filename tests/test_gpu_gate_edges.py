@@ -93,12 +93,18 @@ def nothing(l, idx, score):
     return most < 0.99 * 2.0 ** -150, most < (1.01 * 2.0 ** -126 if score == OG.SOFTMAX else 2.0 ** -148)
 
 
-def share_bound(l, idx):
-    """Relative error of s_j / S: the logit's difference to the largest choice is
-    off by half a step, which exp turns into U * D; exp itself 2, 1 + z and its
-    quotient 2, three rounds of k - 1 additions at most 8, the last quotient 1."""
+def share_bound(l, idx, score):
+    """Relative error of s_j / S.  exp(l - m) by exp2: (2.2 |l - m| + 2) roundings
+    (the difference, its product with log2 e and that constant, each a part of
+    |l - m|; exp2 itself).  Scores of a sum above 2^-64 are those of the row
+    (m its largest logit) or sigmoids (6 roundings at any logit), others are
+    relative to the largest choice.  The error of a score and of the sum, k - 1
+    additions (three rounds of them, at most 8), 1 / sum and the quotient."""
     c = np.take_along_axis(l, idx, 1).astype(np.float64)
-    return ((c.max(axis=1) - c.min(axis=1))[:, None] + 13) * U
+    low = np.take_along_axis(OG.gate_scores(l, score), idx, 1).sum(axis=1) < 1.001 * 2.0 ** -64
+    normal = 6.0 if score == OG.SIGMOID else 2.2 * (l.max(axis=1) - c.min(axis=1)) + 2
+    each = np.where(low, 2.2 * (c.max(axis=1) - c.min(axis=1)) + 2, normal)
+    return (2 * each + 11)[:, None] * U
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
@@ -123,7 +129,7 @@ def test_renormalised_gradient_of_scores_below_fp32(score, k, kind):
         a = 1.5 * np.abs(dw)
         part = np.zeros(l.shape)
         np.put_along_axis(part, idx, p * (a + (a * p).sum(axis=1, keepdims=True)), axis=1)
-        tol = (3 * share_bound(l, idx) + 14 * U) * part + 2.0 ** -149
+        tol = (3 * share_bound(l, idx, score) + 14 * U) * part + 2.0 ** -149
         if given is not None:
             # s (ds - sum ds s) of logits within 5 of the largest or under
             # e^-60: 2 |l - m| + 2 roundings of exp, 10 of the sum, quotient
@@ -159,7 +165,7 @@ def test_renormalised_weights_of_scores_below_fp32(score, k, tie):
     got, w, counts, _ = run_gate(dev(l), bias, *args)
     assert np.array_equal(got, idx) and np.array_equal(counts, ref["counts"])
     must, may = nothing(l, idx, score)
-    ok = (np.abs(w - ref["w"]) <= (share_bound(l, idx) + 2 * U) * ref["w"] + 2.0 ** -149).all(axis=1)
+    ok = (np.abs(w - ref["w"]) <= (share_bound(l, idx, score) + 2 * U) * ref["w"] + 2.0 ** -149).all(axis=1)
     empty = (w == 0).all(axis=1)
     assert np.where(must, empty, ok | (may & empty)).all(), (ok, empty, must, may)
     # every logit -inf: weights 0
