@@ -12,11 +12,11 @@
 // (renormalised: with p_j = s_j / S, dl[e_j] += scale p_j (dw_j - sum_i dw_i p_i),
 // times 1 - s_j for a sigmoid).
 //
-// The order of the experts is that of the exact values: where the fp32 values
-// at the border between chosen and not chosen (of experts or of groups) are
-// nearer to each other than their error, a token is done again with v in 64
-// bits from the fp32 logits.  Without a bias the logits themselves are
-// ordered, and only equal ones need the second look.
+// The order of the experts is that of the values in 64 bits: where the fp32
+// values at the border between chosen and not chosen (of experts or of groups)
+// are nearer to each other than their error, a token is done again with v in 64
+// bits from the logits.  Without a bias the logits themselves are ordered, equal
+// ones in place.
 //
 // The floor is one read of the logits (16.8 MB of fp32 at 16384 x 256: 2.8 us);
 // the selection is what costs, so it is spread over four tokens a wave: 16
@@ -25,10 +25,12 @@
 // then lists of 8 are merged across the lanes (DPP moves); the k-th entry is
 // the threshold that every lane compares its values with.
 //
-// Measured, with the counts' launch, 256 experts of fp32: 16384 tokens 9.7 us,
-// 11.9 with the scores stored (34.6 MB); with a biased sigmoid in 8 groups
-// 21.6, of which 7 are the second look of the few tokens that need one; 128
-// tokens of that 8.2; one token 3.9.
+// Measured, with the counts' launch, 256 experts of fp32, softmax without a bias:
+// 16384 tokens 9.6 us, 11.9 with the scores stored (34.6 MB), one token 3.9 (one
+// launch).  A biased sigmoid in 8 groups: 16384 tokens 21.3 us, of which 7 are the
+// second look of the few that need one; 128 tokens 8.4; one token 6.6, 13.0 with
+// a second look.  With bf16 logits and equal biases 8 % of 16384 tokens tie at the
+// border, up to four of a wave one after the other: 30 to 36 us.
 #include "common.h"
 
 namespace moe {
@@ -746,8 +748,8 @@ __device__ __forceinline__ void store4(uint16_t* p, const float* v) {
 // Lanes and slots as in gate_kernel.  Bound by its reads and writes of [T, E]
 // (16384 x 256 of fp32 with a dense gradient, 51 MB: 10.2 us, 5.0 TB/s);
 // lane j < k of a token has its j-th choice (score from the logit again),
-// whose gradient goes into the row of ds in LDS, each place written once: of
-// an id named twice the first lane adds both.
+// whose gradient goes into the row of ds (renormalised: of dl) in LDS, each place
+// written once: of an id named twice the first lane adds both.
 template <typename D, int LPT, int C>
 __global__ __launch_bounds__(GT) void gate_backward_kernel(GateBwdArgs a) {
   constexpr int TPW = 64 / LPT, V = 4 * C, EMAX = LPT * V, W = GT / 64;

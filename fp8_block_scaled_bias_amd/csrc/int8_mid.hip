@@ -4,8 +4,8 @@
 // Bound by the latency of each K block, where a tile or two a CU is all there
 // is: so the 128-byte K blocks of both operands go through a ring of four
 // stages in LDS, three of them on their way (copies straight into LDS), on
-// across a workgroup's tiles; one barrier a K block.  One group of 256 rows, N
-// = 4096, K = 7168: 42 us (63 with 256 x 256 tiles), of 1024 rows 45 (65).
+// across a workgroup's tiles; one barrier a K block.  One group of 1024 rows, N
+// = 4096, K = 7168: 45 to 50 us (65 with 256 x 256 tiles).
 #include "int8_common.h"
 
 namespace moe {

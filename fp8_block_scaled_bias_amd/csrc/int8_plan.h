@@ -41,7 +41,9 @@ inline int64_t n16(const Shape& s) { return parts(s.N, 16); }
 // there are for the CUs.  Times on 64 groups, N = 4096, K = 7168 (wide / mid /
 // registers): 8 rows 351 / 360 / 317 us, 16: 352 / 360 / 327, 32: 360 / 362 /
 // 374, 128: 420 / 441 / 828; on one group: 16 rows 63 / 38 / 9 us, 64: 63 / 39
-// / 19, 256: 63 / 41 / 30 (256 tiles of 64 x 64), 1024: 65 / 45 / 105.
+// / 19, 256: 63 / 41 / 30 (256 tiles of 64 x 64), 1024: 65 / 45 / 105.  Those are
+// groups of equal size: one that holds most of the rows of a small average is
+// done in tiles of 16 rows, each reading its weights again.
 //
 // Of the register kernels, wider column tiles read a token's row for more
 // weights, narrower ones are more: the widest that still gives every CU one (16

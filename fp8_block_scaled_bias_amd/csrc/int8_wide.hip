@@ -32,10 +32,11 @@
 // end) have an offset outside it, and what their slots hold is not used: such
 // rows are not stored, such K positions are cleared in A's registers.
 //
-// Measured: 8192 x 8192 x 8192 in 414 us, 2.6 POP/s, the matrix cores busy 74 %
-// of the cycles at the 1.58 GHz that the power allows; 256 groups of 512 rows,
-// N = 7168, K = 2048 in 1.84 ms, 2.1 POP/s (65 %, 1.53 GHz); the same with
-// SwiGLU, I = 2048, K = 7168, gathered, in 3.34 ms, 2.3 POP/s.
+// Measured (two cards): 8192 x 8192 x 8192 in 414 to 428 us, 2.6 POP/s, the
+// matrix cores busy 74 to 78 % of the cycles at the 1.56 GHz that the power
+// allows; 256 groups of 512 rows, N = 7168, K = 2048 in 1.84 to 1.90 ms, 2.0 to
+// 2.1 POP/s (65 %); the same with SwiGLU, I = 2048, K = 7168, gathered, in 3.34
+// to 3.48 ms, 2.2 to 2.3 POP/s.
 #include "int8_common.h"
 #include "int8_wide_waits.h"
 

@@ -602,8 +602,8 @@ int moe_router_logits(const void* x_bf16, int64_t T, int64_t H, const float* cen
  *   d_centroids[e, :] = sum_t d_logits[t, e] x[t, :]    (fp32, fixed order)
  * d_logits [T, E] fp32; dx_in_bf16 [T, H] or NULL (0), not aliasing dx_out;
  * workspace: moe_router_backward_dense_workspace_bytes(T, H, E) bytes.
- * Requirements: E % 16 == 0, 16 <= E <= 1024, H % 128 == 0; tensors 16-byte
- * aligned.  T == 0 writes d_centroids = 0.
+ * Requirements: E % 16 == 0, 16 <= E <= 1024, H % 128 == 0, T <= 8388480;
+ * tensors 16-byte aligned.  T == 0 writes d_centroids = 0.
  */
 int moe_router_logits_backward(const void* x_bf16, const float* centroids, const float* d_logits,
                                int64_t T, int64_t H, int32_t E, const void* dx_in_bf16,
@@ -625,8 +625,9 @@ int moe_router_logits_backward(const void* x_bf16, const float* centroids, const
  *                                           0 in fp32)
  *          scale * s[e_j]                   (renormalize 0)
  *   expert_counts[e] = number of tokens that chose e (overwritten).
- * The choice is that of the exact s and v of the given logits and bias: where
- * fp32 values are too close to be told apart they are formed in 64 bits.
+ * The choice is that of s and v of the given logits and bias in 64-bit floating
+ * point (values that are the same there tie: sigmoids of logits above 37, for
+ * one): where fp32 values are too close to be told apart those are formed.
  * A logit of -inf excludes its expert: its score is 0 and it is chosen only
  * where fewer than k others are kept, a row of nothing but -inf has weights 0;
  * so does a bias of -inf, which leaves the score as it is.  Logits of +inf or
