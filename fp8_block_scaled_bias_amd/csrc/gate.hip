@@ -207,7 +207,8 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int64_t t, double*
   for (int i = 0; i < VPL; ++i) {
     const double y = s_v[i * 64 + lane];
     v[i] = a.softmax ? y * inv : (l[i] >= 0.f ? 1.0 : y) / (1.0 + y);
-    s[i] = (float)v[i];
+    // (0 where the first look has 0)
+    s[i] = a.softmax && !(exp_from(l[i], m) > 0.f) ? 0.f : (float)v[i];
   }
   // values of the order; excluded experts (-inf or NaN) below every other,
   // slots that are no candidates at -inf

@@ -202,3 +202,26 @@ def test_more_tokens_than_one_launch_holds():
     # w s (1 - s): w off by its bound, the difference by the parts' roundings
     assert (np.abs(host(dl[at].float()) - want) <= 2.0 ** -8 * np.abs(want) + 200 * U).all()
     assert bool(torch.isfinite(dl).all())
+
+
+@pytest.mark.parametrize("score", [OG.SOFTMAX, OG.SIGMOID])
+def test_weights_and_gradient_are_0_in_the_same_rows(score):
+    """Whether every chosen score is 0 in fp32 does not depend on how the order was
+    found, and the gradient takes the rows whose weights are 0 as such."""
+    k, E = 4, 64
+    l, idx = low_choices(score, k)
+    l = np.concatenate([l, l[:1], l[:1], l[:1]])
+    idx = np.concatenate([idx, idx[:3]])
+    l[7:10, idx[0]] = np.array([-84.5, -91.0, -104.5])[:, None]
+    plain, tied = np.zeros(E, np.float32), np.zeros(E, np.float32)
+    plain[idx[0]] = tied[idx[0]] = tied[-1] = 4.0
+    l[:, -1] = -170.0
+    empty = []
+    for bias in (plain, tied):
+        got, w, _, _ = run_gate(dev(l), bias, score, 1, 1, 1, k, 1, 1.0)
+        assert np.array_equal(got, idx)
+        empty.append((w == 0).all(axis=1))
+    assert np.array_equal(empty[0], empty[1]), empty
+    dw = np.arange(1, 4 * len(l) + 1, dtype=np.float32).reshape(-1, 4) ** 2
+    dl = run_backward(dev(l), score, k, 1, 1.0, idx, dw, None)
+    assert np.array_equal((np.take_along_axis(dl, idx, 1) == 0).all(axis=1), empty[0]), empty
