@@ -1,10 +1,12 @@
 """DeepSeekMoE layer forward on MI355X (gfx950): FP8 block-scaled experts,
 sigmoid + bias group-limited routing, behind the C ABI of libmoe_fp8.so."""
 from . import _lib  # noqa: F401
-from ._lib import (SCORE_SIGMOID, SCORE_SOFTMAX, MoEError, fp8_quant_1x128, fp8_quant_128x128,  # noqa: F401
+from ._lib import (ACT_GELU, ACT_SILU, SCORE_SIGMOID, SCORE_SOFTMAX, MoEError, fp8_quant_1x128, fp8_quant_128x128,  # noqa: F401
                    fp8_quant_128x1_grouped, fp8_transpose_128x128, grouped_fp8_gemm,
                    grouped_fp8_gemm_dgrad,
                    grouped_fp8_gemm_swiglu, grouped_fp8_gemm_swiglu_keep, grouped_fp8_wgrad,
+                   grouped_bf16_gemm, grouped_bf16_gemm_dgrad, grouped_bf16_gemm_dgrad_glu,
+                   grouped_bf16_gemm_glu, grouped_bf16_wgrad,
                    grouped_int8_gemm, grouped_int8_gemm_swiglu, int8_quant_channels,
                    int8_quant_rows, moe_bias_update, moe_combine,
                    moe_combine_backward, moe_gate, moe_gate_backward, moe_permute, moe_permute_noalloc,

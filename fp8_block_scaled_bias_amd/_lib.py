@@ -81,6 +81,13 @@ SIGNATURES = {
                                          _vp, _vp]),
     "grouped_int8_gemm_swiglu": (ctypes.c_int, [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _i32, _i64, _i64,
                                                 _i64, _vp, _vp]),
+    "grouped_bf16_gemm": (ctypes.c_int, [_vp, _vp, _i64, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _vp]),
+    "grouped_bf16_gemm_glu": (ctypes.c_int, [_vp, _vp, _i64, _vp, _vp, _i32, _i64, _i64, _i64, _i32,
+                                             _vp, _vp, _vp]),
+    "grouped_bf16_gemm_dgrad": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _vp]),
+    "grouped_bf16_gemm_dgrad_glu": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32,
+                                                   _vp, _vp]),
+    "grouped_bf16_wgrad": (ctypes.c_int, [_vp, _vp, _vp, _i64, _vp, _i32, _i64, _i64, _i64, _vp, _vp]),
 }
 
 MOE_OK = 0
@@ -89,9 +96,11 @@ MOE_ERR_UNSUPPORTED = -2
 MOE_ERR_HIP = -3
 MOE_ERR_WORKSPACE = -4
 
-# element types and score functions of the gate
+# element types, score functions of the gate
 TYPE_F32, TYPE_BF16 = 0, 1
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+# activations of the gated feed-forward products
+ACT_SILU, ACT_GELU = 0, 1
 
 _lib = None
 
@@ -422,3 +431,39 @@ def grouped_int8_gemm_swiglu(A, A_scale, a_row_index, B, B_scale, group_offsets,
                  _ptr(a_row_index, _i32t, d), _rows(A), _ptr(B, _i8t, d), _ptr(B_scale, _f32t, d),
                  _ptr(group_offsets, _i32t, d), G, M_total, I, K, _ptr(H_bf16, _bf16t, d),
                  _on(stream, d))
+
+
+def grouped_bf16_gemm(A, a_row_index, B, group_offsets, G, M_total, N, K, C_bf16, stream=None):
+    d = _device()
+    return _call("grouped_bf16_gemm", _ptr(A, _bf16t, d), _ptr(a_row_index, _i32t, d), _rows(A),
+                 _ptr(B, _bf16t, d), _ptr(group_offsets, _i32t, d), G, M_total, N, K,
+                 _ptr(C_bf16, _bf16t, d), _on(stream, d))
+
+
+def grouped_bf16_gemm_glu(A, a_row_index, B, group_offsets, G, M_total, I, K, act, H_bf16, GU_bf16=None,
+                          stream=None):
+    d = _device()
+    return _call("grouped_bf16_gemm_glu", _ptr(A, _bf16t, d), _ptr(a_row_index, _i32t, d), _rows(A),
+                 _ptr(B, _bf16t, d), _ptr(group_offsets, _i32t, d), G, M_total, I, K, act,
+                 _ptr(H_bf16, _bf16t, d), _ptr(GU_bf16, _bf16t, d), _on(stream, d))
+
+
+def grouped_bf16_gemm_dgrad(dC, W, group_offsets, G, M_total, N, K, dA_bf16, stream=None):
+    d = _device()
+    return _call("grouped_bf16_gemm_dgrad", _ptr(dC, _bf16t, d), _ptr(W, _bf16t, d),
+                 _ptr(group_offsets, _i32t, d), G, M_total, N, K, _ptr(dA_bf16, _bf16t, d),
+                 _on(stream, d))
+
+
+def grouped_bf16_gemm_dgrad_glu(dC, W, GU, group_offsets, G, M_total, N, I, act, dGU_bf16, stream=None):
+    d = _device()
+    return _call("grouped_bf16_gemm_dgrad_glu", _ptr(dC, _bf16t, d), _ptr(W, _bf16t, d),
+                 _ptr(GU, _bf16t, d), _ptr(group_offsets, _i32t, d), G, M_total, N, I, act,
+                 _ptr(dGU_bf16, _bf16t, d), _on(stream, d))
+
+
+def grouped_bf16_wgrad(dY, A, a_row_index, group_offsets, G, M_total, N, K, dW, stream=None):
+    d = _device()
+    return _call("grouped_bf16_wgrad", _ptr(dY, _bf16t, d), _ptr(A, _bf16t, d),
+                 _ptr(a_row_index, _i32t, d), _rows(A), _ptr(group_offsets, _i32t, d), G, M_total, N, K,
+                 _ptr(dW, _f32t, d), _on(stream, d))

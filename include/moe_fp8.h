@@ -54,6 +54,12 @@ extern "C" {
 #define MOE_SCORE_SOFTMAX    0
 #define MOE_SCORE_SIGMOID    1
 
+/* Activations of the gated feed-forward products (grouped_bf16_gemm_glu):
+ * act(g) = g / (1 + exp(-z)), z = g (SiLU) or 2 sqrt(2/pi) (g + 0.044715 g^3)
+ * (the tanh form of GELU). */
+#define MOE_ACT_SILU         0
+#define MOE_ACT_GELU         1
+
 /* Message of the last failed call on this thread ("" if none). */
 const char* moe_last_error(void);
 
@@ -724,6 +730,78 @@ int grouped_int8_gemm_swiglu(const int8_t* A, const float* A_scale, const int32_
                              int64_t A_rows, const int8_t* B, const float* B_scale,
                              const int32_t* group_offsets, int32_t G, int64_t M_total, int64_t I,
                              int64_t K, void* H_bf16, void* stream);
+
+/*
+ * grouped_bf16_gemm - grouped product of bf16 matrices: experts that are not
+ * quantised (G = 1: a linear layer).  For group g, rows r in
+ * [group_offsets[g], group_offsets[g+1]):
+ *   C[r, n] = bf16( sum_k A[src, k] * B[g, n, k] )       (fp32 sums)
+ * src = a_row_index[r] if that is not NULL, else r.
+ *
+ * A        [A_rows, K] bf16
+ * a_row_index [M_total] int32 or NULL, A_rows: as in grouped_fp8_gemm
+ * B        [G, N, K] bf16 (K contiguous)
+ * group_offsets [G+1] int32 on the device, non-decreasing, [0] == 0, [G] <=
+ *          M_total; rows from [G] on are left as they were
+ * C  (out) [M_total, N] bf16
+ * An infinity or NaN reaches the results that it takes part in and no others.
+ * Requirements of all grouped bf16 products: N, K (I) multiples of 8, at most
+ * 2^21; 1 <= G <= 1024; tensors 16-byte aligned.  M_total == 0 is a no-op
+ * (grouped_bf16_wgrad writes dW = 0).
+ */
+int grouped_bf16_gemm(const void* A_bf16, const int32_t* a_row_index, int64_t A_rows,
+                      const void* B_bf16, const int32_t* group_offsets, int32_t G, int64_t M_total,
+                      int64_t N, int64_t K, void* C_bf16, void* stream);
+
+/*
+ * grouped_bf16_gemm_glu - both projections of the gated feed-forward block, the
+ * activation and the product in one kernel.  B holds each group's fused
+ * weight [2I, K]: rows [0, I) gate, [I, 2I) up.  With the fp32 sums gt and ut
+ * that grouped_bf16_gemm (N = 2I) rounds to C:
+ *   H[r, c] = bf16( act(gt) * ut )   (fp32);  act MOE_ACT_SILU or MOE_ACT_GELU
+ * H_bf16 (out) [M_total, I]; GU_bf16 (out, optional: NULL skips it) [M_total,
+ * 2I] = bf16 [gt | ut], what grouped_bf16_gemm_dgrad_glu reads.
+ */
+int grouped_bf16_gemm_glu(const void* A_bf16, const int32_t* a_row_index, int64_t A_rows,
+                          const void* B_bf16, const int32_t* group_offsets, int32_t G,
+                          int64_t M_total, int64_t I, int64_t K, int32_t act, void* H_bf16,
+                          void* GU_bf16, void* stream);
+
+/*
+ * grouped_bf16_gemm_dgrad - the input gradient of grouped_bf16_gemm, from the
+ * weights as stored (no transposed copy):
+ *   dA[r, k] = bf16( sum_n dC[r, n] * W[g, n, k] )       (fp32 sums)
+ * dC [M_total, N] bf16; W [G, N, K] bf16; dA (out) [M_total, K] bf16.  With a
+ * row gather in the forward, dA's rows are the gathered ones (moe_combine with
+ * unit weights adds them up for each token).
+ */
+int grouped_bf16_gemm_dgrad(const void* dC_bf16, const void* W_bf16, const int32_t* group_offsets,
+                            int32_t G, int64_t M_total, int64_t N, int64_t K, void* dA_bf16,
+                            void* stream);
+
+/*
+ * grouped_bf16_gemm_dgrad_glu - grouped_bf16_gemm_dgrad of the down projection
+ * W [G, N, I] with the gated activation's backward in its epilogue: with dh the
+ * fp32 sum that grouped_bf16_gemm_dgrad (K = I) rounds, g and u from GU_bf16
+ * [M_total, 2I] = [g | u] (grouped_bf16_gemm_glu's),
+ *   dGU[r, c]     = bf16( dh * u * act'(g) )
+ *   dGU[r, I + c] = bf16( dh * act(g) )                  (fp32)
+ * dGU_bf16 (out) [M_total, 2I], not aliasing GU_bf16.
+ */
+int grouped_bf16_gemm_dgrad_glu(const void* dC_bf16, const void* W_bf16, const void* GU_bf16,
+                                const int32_t* group_offsets, int32_t G, int64_t M_total, int64_t N,
+                                int64_t I, int32_t act, void* dGU_bf16, void* stream);
+
+/*
+ * grouped_bf16_wgrad - each group's weight gradient:
+ *   dW[g, n, k] = sum_{r of group g} dY[r, n] * A[src(r), k]     (fp32)
+ * summed in ascending order of rows, in steps of the matrix instruction.
+ * dY [M_total, N] bf16; A [A_rows, K] bf16 with a_row_index as in
+ * grouped_bf16_gemm; dW (out) [G, N, K] fp32, 0 for a group without rows.
+ */
+int grouped_bf16_wgrad(const void* dY_bf16, const void* A_bf16, const int32_t* a_row_index,
+                       int64_t A_rows, const int32_t* group_offsets, int32_t G, int64_t M_total,
+                       int64_t N, int64_t K, float* dW, void* stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */

@@ -327,3 +327,38 @@ def test_int8_validation():
         assert g(a=None) == L.MOE_ERR_INVALID and g(out=None) == L.MOE_ERR_INVALID
         assert g(a=ctypes.c_void_p(4104)) == L.MOE_ERR_INVALID and "aligned" in L.last_error()
         assert g(M=0, a=None, out=None) == L.MOE_OK
+
+
+def test_bf16_products_validation():
+    odd, B, OUT = ctypes.c_void_p(4104), ctypes.c_void_p(16384), ctypes.c_void_p(12288)
+    calls = {
+        "grouped_bf16_gemm": lambda G=2, M=8, N=64, K=64, rows=8, idx=None, a=FAKE, b=B, o=OUT, act=0:
+            rc("grouped_bf16_gemm", a, idx, rows, b, FAKE, G, M, N, K, o, None),
+        "grouped_bf16_gemm_glu": lambda G=2, M=8, N=64, K=64, rows=8, idx=None, a=FAKE, b=B, o=OUT, act=0:
+            rc("grouped_bf16_gemm_glu", a, idx, rows, b, FAKE, G, M, N, K, act, o, None, None),
+        "grouped_bf16_gemm_dgrad": lambda G=2, M=8, N=64, K=64, rows=8, idx=None, a=FAKE, b=B, o=OUT, act=0:
+            rc("grouped_bf16_gemm_dgrad", a, b, FAKE, G, M, N, K, o, None),
+        "grouped_bf16_gemm_dgrad_glu": lambda G=2, M=8, N=64, K=64, rows=8, idx=None, a=FAKE, b=B, o=OUT, act=0:
+            rc("grouped_bf16_gemm_dgrad_glu", a, b, ctypes.c_void_p(8192), FAKE, G, M, N, K, act, o, None),
+        "grouped_bf16_wgrad": lambda G=2, M=8, N=64, K=64, rows=8, idx=None, a=FAKE, b=B, o=OUT, act=0:
+            rc("grouped_bf16_wgrad", a, b, idx, rows, FAKE, G, M, N, K, o, None),
+    }
+    for name, f in calls.items():
+        for bad in (dict(G=0), dict(M=-1), dict(N=60), dict(N=0), dict(K=4), dict(K=-8)):
+            assert f(**bad) == L.MOE_ERR_INVALID and name in L.last_error(), (name, bad)
+        for bad in (dict(G=1025), dict(N=(1 << 21) + 8), dict(K=(1 << 21) + 8)):
+            assert f(**bad) == L.MOE_ERR_UNSUPPORTED, (name, bad)
+        for p in "abo":
+            assert f(**{p: None}) == L.MOE_ERR_INVALID and "null" in L.last_error(), (name, p)
+            assert f(**{p: odd}) == L.MOE_ERR_INVALID and "aligned" in L.last_error(), (name, p)
+        assert f(o=FAKE) == L.MOE_ERR_INVALID and f(o=B) == L.MOE_ERR_INVALID and "alias" in L.last_error()
+        if name != "grouped_bf16_wgrad":
+            assert f(M=0, a=None, b=None, o=None, rows=0) == L.MOE_OK
+        if "glu" in name:
+            assert f(act=2) == L.MOE_ERR_INVALID and "act=2" in L.last_error()
+    for name in ("grouped_bf16_gemm", "grouped_bf16_gemm_glu", "grouped_bf16_wgrad"):
+        assert calls[name](rows=7) == L.MOE_ERR_INVALID and "A_rows" in L.last_error()
+        assert calls[name](rows=0, idx=FAKE) == L.MOE_ERR_INVALID
+        assert calls[name](rows=4, idx=ctypes.c_void_p(4098)) == L.MOE_ERR_INVALID
+    assert rc("grouped_bf16_gemm_dgrad_glu", FAKE, FAKE, FAKE, FAKE, 2, 8, 64, 64, 0, FAKE, None) == \
+        L.MOE_ERR_INVALID and "alias" in L.last_error()
