@@ -88,6 +88,16 @@ SIGNATURES = {
     "grouped_bf16_gemm_dgrad_glu": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32,
                                                    _vp, _vp]),
     "grouped_bf16_wgrad": (ctypes.c_int, [_vp, _vp, _vp, _i64, _vp, _i32, _i64, _i64, _i64, _vp, _vp]),
+    "moe_norm": (ctypes.c_int, [_vp, _i32, _vp, _vp, _i64, _i64, _f32, _vp, _vp, _vp, _i32, _vp, _vp, _vp]),
+    "moe_norm_backward_workspace_bytes": (_sz, [_i64, _i64]),
+    "moe_norm_backward": (ctypes.c_int, [_vp, _vp, _i32, _vp, _vp, _vp, _f32, _i64, _i64, _vp, _vp, _vp,
+                                         _sz, _vp]),
+    "moe_combine_norm": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _f32, _i32, _vp, _f32, _f32,
+                                        _i64, _i32, _i64, _vp, _vp, _vp]),
+    "moe_combine_norm_backward_workspace_bytes": (_sz, [_i64, _i64]),
+    "moe_combine_norm_backward": (ctypes.c_int, [_vp, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _f32, _f32,
+                                                 _i64, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                                                 _vp]),
 }
 
 MOE_OK = 0
@@ -101,6 +111,8 @@ TYPE_F32, TYPE_BF16 = 0, 1
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 # activations of the gated feed-forward products
 ACT_SILU, ACT_GELU = 0, 1
+# codes that moe_norm writes
+QUANT_NONE, QUANT_E4M3, QUANT_INT8 = 0, 1, 2
 
 _lib = None
 
@@ -363,9 +375,9 @@ def _on(stream, dev):
     return _raw_stream(dev) if stream is None else _stream(stream)
 
 
-def _logits_type(t):
+def _logits_type(t, what="logits"):
     if not isinstance(t, _Tensor) or t.dtype not in (_f32t, _bf16t):
-        raise TypeError("logits must be a float32 or bfloat16 torch.Tensor")
+        raise TypeError(f"{what} must be a float32 or bfloat16 torch.Tensor")
     return TYPE_F32 if t.dtype == _f32t else TYPE_BF16
 
 
@@ -467,3 +479,56 @@ def grouped_bf16_wgrad(dY, A, a_row_index, group_offsets, G, M_total, N, K, dW, 
     return _call("grouped_bf16_wgrad", _ptr(dY, _bf16t, d), _ptr(A, _bf16t, d),
                  _ptr(a_row_index, _i32t, d), _rows(A), _ptr(group_offsets, _i32t, d), G, M_total, N, K,
                  _ptr(dW, _f32t, d), _on(stream, d))
+
+
+_u8t = torch.uint8
+_CODES = {QUANT_E4M3: _u8t, QUANT_INT8: _i8t}
+
+
+def moe_norm(x, add_bf16, weight, T, H, eps, sum_out, n_bf16, rstd=None, quant=QUANT_NONE, codes=None,
+             scales=None, stream=None):
+    d = _device()
+    kind = _logits_type(x, "x")
+    return _call("moe_norm", _ptr(x, None, d), kind, _ptr(add_bf16, _bf16t, d), _ptr(weight, _f32t, d), T, H,
+                 eps, _ptr(sum_out, x.dtype, d), _ptr(n_bf16, _bf16t, d), _ptr(rstd, _f32t, d), quant,
+                 _ptr(codes, _CODES.get(quant), d), _ptr(scales, _f32t, d), _on(stream, d))
+
+
+def moe_norm_backward_workspace_bytes(T, H) -> int:
+    return int(lib().moe_norm_backward_workspace_bytes(T, H))
+
+
+def moe_norm_backward(dn_bf16, x, weight, rstd, d_res, res_scale, T, H, dx, d_weight, workspace,
+                      workspace_bytes, stream=None):
+    d = _device()
+    kind = _logits_type(x, "x")
+    return _call("moe_norm_backward", _ptr(dn_bf16, _bf16t, d), _ptr(x, None, d), kind, _ptr(weight, _f32t, d),
+                 _ptr(rstd, _f32t, d), _ptr(d_res, x.dtype, d), res_scale, T, H, _ptr(dx, x.dtype, d),
+                 _ptr(d_weight, _f32t, d), _ptr(workspace, None, d), workspace_bytes, _on(stream, d))
+
+
+def moe_combine_norm(expert_out_bf16, inv_perm, topk_w, shared_out_bf16, shared_w, residual, residual_scale,
+                     norm, weight, eps, scale, T, k, H, y, rstd=None, stream=None):
+    d = _device()
+    kind = _logits_type(residual, "residual")
+    return _call("moe_combine_norm", _ptr(expert_out_bf16, _bf16t, d), _ptr(inv_perm, _i32t, d),
+                 _ptr(topk_w, _f32t, d), _ptr(shared_out_bf16, _bf16t, d), _ptr(shared_w, _f32t, d),
+                 _ptr(residual, None, d), kind, residual_scale, int(norm), _ptr(weight, _f32t, d), eps, scale,
+                 T, k, H, _ptr(y, residual.dtype, d), _ptr(rstd, _f32t, d), _on(stream, d))
+
+
+def moe_combine_norm_backward_workspace_bytes(T, H) -> int:
+    return int(lib().moe_combine_norm_backward_workspace_bytes(T, H))
+
+
+def moe_combine_norm_backward(dy, inv_perm, topk_w, expert_out_bf16, n_shared, shared_w, norm, weight, eps,
+                              scale, T, k, H, d_expert_out_bf16, d_topk_w, d_shared_w, d_expert_out_e4m3,
+                              d_expert_out_scale, d_weight, workspace, workspace_bytes, stream=None):
+    d = _device()
+    kind = _logits_type(dy, "dy")
+    return _call("moe_combine_norm_backward", _ptr(dy, None, d), kind, _ptr(inv_perm, _i32t, d),
+                 _ptr(topk_w, _f32t, d), _ptr(expert_out_bf16, _bf16t, d), n_shared, _ptr(shared_w, _f32t, d),
+                 int(norm), _ptr(weight, _f32t, d), eps, scale, T, k, H, _ptr(d_expert_out_bf16, _bf16t, d),
+                 _ptr(d_topk_w, _f32t, d), _ptr(d_shared_w, _f32t, d), _ptr(d_expert_out_e4m3, _u8t, d),
+                 _ptr(d_expert_out_scale, _f32t, d), _ptr(d_weight, _f32t, d), _ptr(workspace, None, d),
+                 workspace_bytes, _on(stream, d))

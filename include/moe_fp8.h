@@ -60,6 +60,14 @@ extern "C" {
 #define MOE_ACT_SILU         0
 #define MOE_ACT_GELU         1
 
+/* Codes that moe_norm writes beside the normed rows. */
+#define MOE_QUANT_NONE       0
+#define MOE_QUANT_E4M3       1   /* 1x128 tiles, as fp8_quant_1x128 */
+#define MOE_QUANT_INT8       2   /* one scale a row, as int8_quant_rows */
+
+/* Most parts that a backward norm keeps of d_weight (workspace rows). */
+#define MOE_NORM_MAX_PARTS   512
+
 /* Message of the last failed call on this thread ("" if none). */
 const char* moe_last_error(void);
 
@@ -802,6 +810,101 @@ int grouped_bf16_gemm_dgrad_glu(const void* dC_bf16, const void* W_bf16, const v
 int grouped_bf16_wgrad(const void* dY_bf16, const void* A_bf16, const int32_t* a_row_index,
                        int64_t A_rows, const int32_t* group_offsets, int32_t G, int64_t M_total,
                        int64_t N, int64_t K, float* dW, void* stream);
+
+/*
+ * moe_norm - the norm before a block: the residual add, the RMS norm and the
+ * codes that the block's first product reads, in one pass.  For each row t:
+ *   v       = x[t, :] + add[t, :]     stored to sum_out in x's type (rounded to
+ *                                     nearest even; what is stored is normed);
+ *             x[t, :] without an add
+ *   rstd[t] = 1 / sqrt( (1/H) sum_h v[h]^2 + eps )
+ *   n[t, h] = bf16( v[h] * rstd[t] * weight[h] )
+ * and from the fp32 products v * rstd * weight, before their rounding to bf16:
+ *   MOE_QUANT_E4M3  codes [T, H] e4m3, scales [T, H/128]: fp8_quant_1x128's rule
+ *   MOE_QUANT_INT8  codes [T, H] int8, scales [T]: int8_quant_rows' rule, the
+ *                   quotient rounded to fp32 before it is to a whole number
+ * in fp32: a row's squares have to stay under the largest fp32 number.
+ * x        [T, H] fp32 or bf16 (x_type MOE_TYPE_*)
+ * add_bf16 [T, H] bf16 or NULL;  sum_out (out) [T, H] of x_type, given if and
+ *          only if add is; may equal x
+ * weight   [H] fp32, or NULL (1)
+ * n_bf16   (out) [T, H];  rstd (out, optional: NULL skips it) [T] fp32
+ * Requirements: H % 8 == 0 (% 128 with E4M3 codes), H <= 16384, T < 2^28, 0 <=
+ * eps <= 1; tensors 16-byte, codes 8-byte aligned.  T == 0 is a no-op.
+ */
+int moe_norm(const void* x, int32_t x_type, const void* add_bf16, const float* weight, int64_t T,
+             int64_t H, float eps, void* sum_out, void* n_bf16, float* rstd, int32_t quant, void* codes,
+             float* scales, void* stream);
+
+/*
+ * moe_norm_backward - the gradient of moe_norm's n to its normed rows v (and so
+ * to x and add alike), with what comes down the residual path beside it:
+ *   hat = v[t, :] * rstd[t];  g = dn[t, :] * weight
+ *   dx[t, :]    = res_scale * d_res[t, :] + rstd[t] * (g - hat * (1/H) sum_h g hat)
+ *   d_weight[h] = sum_t dn[t, h] * hat[t, h]        (fp32, in a fixed order)
+ * dn_bf16 [T, H]; x [T, H] of x_type: v as stored (sum_out, or x without an
+ * add); rstd [T]: moe_norm's; d_res [T, H] of x_type or NULL (0); dx (out)
+ * [T, H] of x_type, may equal d_res; d_weight (out) [H] fp32, or NULL to skip
+ * it; weight [H] or NULL (1).
+ * workspace: moe_norm_backward_workspace_bytes(T, H) bytes, 16-byte aligned
+ * (NULL without d_weight); calls that overlap need one each.
+ * Requirements: as moe_norm's.  T == 0 writes d_weight = 0.
+ */
+size_t moe_norm_backward_workspace_bytes(int64_t T, int64_t H);
+int moe_norm_backward(const void* dn_bf16, const void* x, int32_t x_type, const float* weight,
+                      const float* rstd, const void* d_res, float res_scale, int64_t T, int64_t H,
+                      void* dx, float* d_weight, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_combine_norm - the end of a block: moe_combine's gate-weighted sum, a norm
+ * after it and the scaled residual sum, in one pass.  For each token:
+ *   z = sum_{j<k} topk_w[t, j] * D[inv_perm[t*k + j], :] + shared_w[t] * S[t, :]
+ *   b = z * rstd[t] * weight,  rstd[t] = 1 / sqrt( (1/H) sum_h z[h]^2 + eps )
+ *       (norm 0: rstd = 1, weight a scale for each channel)
+ *   y[t, :] = residual_scale * residual[t, :] + scale * b
+ * in fp32, z in slot order and never rounded; y rounded once to x_type.
+ * D [R, H] bf16 (R >= T*k), inv_perm [T*k] (an entry outside [0, T*k) reads row
+ * T*k - 1), topk_w [T, k], S [T, H] bf16 or NULL: as in moe_combine
+ * shared_w  [T] fp32 or NULL (1): the shared expert's own gate
+ * residual  [T, H] of x_type (MOE_TYPE_*);  weight [H] fp32 or NULL (1)
+ * y (out)   [T, H] of x_type, may equal residual;  rstd (out, optional) [T]
+ *           fp32, written with norm 1
+ * Requirements: 1 <= k <= 8; H % 8 == 0, H <= 16384; T < 2^28; 0 <= eps <= 1;
+ * tensors 16-byte aligned.  T == 0 is a no-op.
+ */
+int moe_combine_norm(const void* expert_out_bf16, const int32_t* inv_perm, const float* topk_w,
+                     const void* shared_out_bf16, const float* shared_w, const void* residual,
+                     int32_t x_type, float residual_scale, int32_t norm, const float* weight, float eps,
+                     float scale, int64_t T, int32_t k, int64_t H, void* y, float* rstd, void* stream);
+
+/*
+ * moe_combine_norm_backward - backward of moe_combine_norm but for the residual's
+ * part (residual_scale * dy, which moe_norm_backward adds as d_res).  z and
+ * rstd are formed again from D, bit for bit; with hat = z * rstd, g = scale *
+ * dy[t, :]:
+ *   d_weight[h] = sum_t g * hat                      (fp32, in a fixed order)
+ *   dz          = rstd * (g * weight - hat * (1/H) sum_h g * weight * hat)
+ *                 (norm 0: g * weight)
+ *   dD[inv_perm[t*k + j], :] = bf16( topk_w[t, j] * dz ),  d_topk_w[t, j] = <dz, D[..]>
+ *   dD[T*k + t, :] = bf16( shared_w[t] * dz ),  d_shared_w[t] = <dz, D[T*k + t, :]>
+ * dy [T, H] of x_type; D, dD (out) [T*k + n_shared*T, H] bf16; d_topk_w (out)
+ * [T, k], d_shared_w (out, optional) [T] fp32; d_weight (out, optional) [H].
+ * inv_perm entries outside [0, T*k) read row T*k - 1 and are not written.
+ * d_expert_out_e4m3, d_expert_out_scale (out, both or neither): the 1x128
+ * quantisation of dD, as in moe_combine_backward but of the fp32 products
+ * before their rounding to bf16; needs H % 128 == 0.
+ * workspace: moe_combine_norm_backward_workspace_bytes(T, H) bytes, as
+ * moe_norm_backward's.  Requirements: as moe_combine_norm's, n_shared in {0,
+ * 1}.  T == 0 writes d_weight = 0.
+ */
+size_t moe_combine_norm_backward_workspace_bytes(int64_t T, int64_t H);
+int moe_combine_norm_backward(const void* dy, int32_t x_type, const int32_t* inv_perm,
+                              const float* topk_w, const void* expert_out_bf16, int32_t n_shared,
+                              const float* shared_w, int32_t norm, const float* weight, float eps,
+                              float scale, int64_t T, int32_t k, int64_t H, void* d_expert_out_bf16,
+                              float* d_topk_w, float* d_shared_w, uint8_t* d_expert_out_e4m3,
+                              float* d_expert_out_scale, float* d_weight, void* workspace,
+                              size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */

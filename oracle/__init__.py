@@ -28,10 +28,11 @@ What each module computes, and the passage it follows:
 * ``int8``     - quantisation by rows and the grouped product in 8-bit integers.
 * ``bf16``     - grouped products of bf16 experts, the gated activations and
   their gradients.
+* ``norm``     - the norms before and after a block and their gradients.
 * ``layer``    - the whole forward, and a per-token direct form used as a pin.
 
 Parity pins: every function here is pinned in ``tests/test_oracle_*.py``.
 Parity unpinned by the pages: the pages print no worked example, so every
 pin is a closed form, an invariant, a brute force or a library cross-check.
 """
-from . import formats, quant, route, balance, permute, gemm, swiglu, combine, gate, int8, bf16, layer  # noqa: F401
+from . import formats, quant, route, balance, permute, gemm, swiglu, combine, gate, int8, bf16, norm, layer  # noqa: F401

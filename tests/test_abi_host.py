@@ -362,3 +362,62 @@ def test_bf16_products_validation():
         assert calls[name](rows=4, idx=ctypes.c_void_p(4098)) == L.MOE_ERR_INVALID
     assert rc("grouped_bf16_gemm_dgrad_glu", FAKE, FAKE, FAKE, FAKE, 2, 8, 64, 64, 0, FAKE, None) == \
         L.MOE_ERR_INVALID and "alias" in L.last_error()
+
+
+def test_norm_validation():
+    odd = ctypes.c_void_p(4104)
+    P = [ctypes.c_void_p(16384 * i) for i in range(1, 12)]
+
+    def n(x=P[0], t=1, add=None, w=None, T=4, H=128, eps=1e-6, s=None, o=P[1], r=None, q=0, c=None, sc=None):
+        return rc("moe_norm", x, t, add, w, T, H, eps, s, o, r, q, c, sc, None)
+
+    def nb(dn=P[0], x=P[1], t=1, w=None, r=P[2], res=None, T=4, H=128, dx=P[3], dw=None, ws=None, b=0):
+        return rc("moe_norm_backward", dn, x, t, w, r, res, 1.0, T, H, dx, dw, ws, b, None)
+
+    def c(D=P[0], i=P[1], w=P[2], S=None, sw=None, x=P[3], t=1, norm=1, wt=None, eps=1e-6, T=4, k=2, H=128, y=P[4]):
+        return rc("moe_combine_norm", D, i, w, S, sw, x, t, 1.0, norm, wt, eps, 1.0, T, k, H, y, None, None)
+
+    def cb(dy=P[0], t=1, i=P[1], w=P[2], D=P[3], ns=0, sw=None, norm=1, wt=None, eps=1e-6, T=4, k=2, H=128, dD=P[4],
+           dw=P[5], dsw=None, q=None, qs=None, dwt=None, ws=None, b=0):
+        return rc("moe_combine_norm_backward", dy, t, i, w, D, ns, sw, norm, wt, eps, 1.0, T, k, H, dD, dw, dsw, q, qs,
+                  dwt, ws, b, None)
+    for name, f in (("moe_norm", n), ("moe_norm_backward", nb), ("moe_combine_norm", c), ("moe_combine_norm_backward", cb)):
+        for bad in (dict(T=-1), dict(T=1 << 28), dict(H=0), dict(H=100), dict(t=2)):
+            assert f(**bad) == L.MOE_ERR_INVALID and name in L.last_error(), (name, bad)
+        assert f(H=16392) == L.MOE_ERR_UNSUPPORTED
+    nan = float("nan")
+    for f in (n, c, cb):
+        for eps in (-1.0, 2.0, nan):
+            assert f(eps=eps) == L.MOE_ERR_INVALID and "eps" in L.last_error()
+    assert n(q=3) == L.MOE_ERR_INVALID and n(q=-1) == L.MOE_ERR_INVALID
+    assert n(q=1, H=136, c=P[2], sc=P[3]) == L.MOE_ERR_INVALID and "128" in L.last_error()
+    assert n(add=P[2]) == L.MOE_ERR_INVALID and n(s=P[2]) == L.MOE_ERR_INVALID and "together" in L.last_error()
+    assert n(q=1) == L.MOE_ERR_INVALID and "null" in L.last_error()
+    assert n(q=2, c=P[2], sc=None) == L.MOE_ERR_INVALID and n(x=None) == L.MOE_ERR_INVALID
+    assert n(x=odd) == L.MOE_ERR_INVALID and n(w=odd) == L.MOE_ERR_INVALID and "aligned" in L.last_error()
+    assert n(o=P[0]) == L.MOE_ERR_INVALID and "alias" in L.last_error()
+    assert n(T=0, x=None, o=None) == L.MOE_OK
+    for p in ("dn", "x", "r", "dx"):
+        assert nb(**{p: None}) == L.MOE_ERR_INVALID and "null" in L.last_error()
+    assert nb(dn=odd) == L.MOE_ERR_INVALID and "aligned" in L.last_error()
+    assert nb(dx=P[0]) == L.MOE_ERR_INVALID and nb(dx=P[1]) == L.MOE_ERR_INVALID and "alias" in L.last_error()
+    need = rc("moe_norm_backward_workspace_bytes", 4, 128)
+    assert need == 4 * 128 * 4 and rc("moe_norm_backward_workspace_bytes", 1 << 20, 128) == 512 * 128 * 4
+    assert rc("moe_combine_norm_backward_workspace_bytes", 4, 128) == need
+    assert nb(dw=P[4], ws=P[5], b=need - 1) == L.MOE_ERR_WORKSPACE and str(need) in L.last_error()
+    assert nb(dw=P[4]) == L.MOE_ERR_WORKSPACE
+    assert nb(T=0, dn=None, x=None, r=None, dx=None) == L.MOE_OK
+    for f in (c, cb):
+        for bad in (dict(k=0), dict(k=9), dict(norm=2), dict(D=None), dict(i=None), dict(w=None), dict(D=odd)):
+            assert f(**bad) == L.MOE_ERR_INVALID, bad
+    assert c(sw=P[5]) == L.MOE_ERR_INVALID and "shared" in L.last_error()
+    assert c(x=None) == L.MOE_ERR_INVALID and c(y=None) == L.MOE_ERR_INVALID
+    assert c(y=P[0]) == L.MOE_ERR_INVALID and "alias" in L.last_error()
+    assert c(T=0, D=None, i=None, w=None, x=None, y=None) == L.MOE_OK
+    assert cb(ns=2) == L.MOE_ERR_INVALID
+    assert cb(sw=P[6]) == L.MOE_ERR_INVALID and cb(dsw=P[6]) == L.MOE_ERR_INVALID and "shared" in L.last_error()
+    assert cb(q=P[6]) == L.MOE_ERR_INVALID and "together" in L.last_error()
+    assert cb(q=P[6], qs=P[7], H=136) == L.MOE_ERR_INVALID and "128" in L.last_error()
+    assert cb(dD=P[3]) == L.MOE_ERR_INVALID and "alias" in L.last_error()
+    assert cb(dwt=P[6], ws=P[7], b=need - 1) == L.MOE_ERR_WORKSPACE
+    assert cb(T=0, dy=None, i=None, w=None, D=None, dD=None, dw=None) == L.MOE_OK
