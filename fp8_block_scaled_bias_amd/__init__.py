@@ -19,5 +19,6 @@ from ._lib import (ACT_GELU, ACT_SILU, QUANT_E4M3, QUANT_INT8, QUANT_NONE, SCORE
                    moe_router_dcentroids, moe_router_logits, moe_router_logits_backward,
                    moe_seq_balance, moe_seq_balance_workspace_bytes,
                    swiglu_backward, swiglu_backward_grouped, wgrad_chunks)
-from .layer import (BackwardBuffers, Buffers, Gate, Int8Buffers, Int8MoELayer, LayerShape,  # noqa: F401
+from .layer import (BackwardBuffers, Bf16BackwardBuffers, Bf16Buffers, Bf16MoELayer,  # noqa: F401
+                    BlockBuffers, Buffers, Gate, Int8Buffers, Int8MoELayer, LayerShape, MoEBlock,
                     MoELayer)

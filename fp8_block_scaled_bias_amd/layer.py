@@ -59,8 +59,23 @@ for each token and each output channel):
   6. grouped_int8_gemm      down projection
   7. moe_combine
 
-torch is only used to hold device memory and to name the stream; every step
-runs in the library's HIP kernels.
+Bf16MoELayer is the layer, forward and backward, on unquantised experts:
+
+  1. the router and moe_permute, as above
+  2. grouped_bf16_gemm_glu  h = act(gate) up, gathered x (its gate and up
+                            outputs kept on demand)
+  3. grouped_bf16_gemm      down projection
+  4. moe_combine
+  and backward moe_combine_backward, grouped_bf16_gemm_dgrad_glu (down, with the
+  activation's backward), grouped_bf16_gemm_dgrad (gate and up), moe_combine,
+  grouped_bf16_wgrad twice, the router's as above.
+
+MoEBlock is one of these layers between its norms, on the residual stream:
+moe_norm in front (in place of the operand's quantisation), moe_combine_norm at
+the end (in place of moe_combine), and their backward.
+
+torch is only used to hold device memory, to name the stream and to round new
+bf16 weights; every step runs in the library's HIP kernels.
 """
 from __future__ import annotations
 
@@ -201,11 +216,27 @@ class BackwardBuffers:
         s = shape
         R = T * s.k + s.n_shared * T
         dev = torch.device(device)
-        u8, f32, bf = torch.uint8, torch.float32, torch.bfloat16
+        f32, bf = torch.float32, torch.bfloat16
         H, I = s.H, s.I
         self.T, self.R = T, R
         self.dD = torch.empty((R, H), dtype=bf, device=dev)
         self.dw = torch.empty((T, s.k), dtype=f32, device=dev)
+        self.dxp = torch.empty((R, H), dtype=bf, device=dev)
+        self.dx = torch.empty((T, H), dtype=bf, device=dev)
+        self.ones = torch.ones((T, s.k), dtype=f32, device=dev)
+        self.dW_gu = torch.empty((s.G, 2 * I, H), dtype=f32, device=dev)
+        self.dW_dn = torch.empty((s.G, H, I), dtype=f32, device=dev)
+        self.dx_total = torch.empty((T, H), dtype=bf, device=dev)
+        self._shape, self._dev, self.dlogit = s, dev, None
+        self.dlogit_rows = torch.empty((max(T * s.k, 1),), dtype=f32, device=dev)
+        self.dC = torch.empty((s.E, H), dtype=f32, device=dev)
+        self._operands()
+
+    def _operands(self):
+        """What only the products in E4M3 read and write."""
+        s, R, dev = self._shape, self.R, self._dev
+        u8, f32, bf = torch.uint8, torch.float32, torch.bfloat16
+        H, I = s.H, s.I
         self.dDq = torch.empty((R, H), dtype=u8, device=dev)
         self.dDs = torch.empty((R, H // 128), dtype=f32, device=dev)
         self.dh = torch.empty((R, I), dtype=bf, device=dev)
@@ -213,11 +244,7 @@ class BackwardBuffers:
         self.dgu = self.h = None   # bf16 dGU and h: only with keep_intermediates
         self.dguq = torch.empty((R, 2 * I), dtype=u8, device=dev)
         self.dgus = torch.empty((R, 2 * I // 128), dtype=f32, device=dev)
-        self.dxp = torch.empty((R, H), dtype=bf, device=dev)
-        self.dx = torch.empty((T, H), dtype=bf, device=dev)
-        self.ones = torch.ones((T, s.k), dtype=f32, device=dev)
-        self.cap = L.wgrad_chunks(R, s.G)
-        c = self.cap
+        c = self.cap = L.wgrad_chunks(R, s.G)
         self.c_dD = torch.empty((c, H, 128), dtype=u8, device=dev)
         self.s_dD = torch.empty((c, H), dtype=f32, device=dev)
         self.c_h = torch.empty((c, I, 128), dtype=u8, device=dev)
@@ -226,12 +253,11 @@ class BackwardBuffers:
         self.s_dgu = torch.empty((c, 2 * I), dtype=f32, device=dev)
         self.c_x = torch.empty((c, H, 128), dtype=u8, device=dev)
         self.s_x = torch.empty((c, H), dtype=f32, device=dev)
-        self.dW_gu = torch.empty((s.G, 2 * I, H), dtype=f32, device=dev)
-        self.dW_dn = torch.empty((s.G, H, I), dtype=f32, device=dev)
-        self.dx_total = torch.empty((T, H), dtype=bf, device=dev)
-        self._shape, self._dev, self.dlogit = s, dev, None
-        self.dlogit_rows = torch.empty((max(T * s.k, 1),), dtype=f32, device=dev)
-        self.dC = torch.empty((s.E, H), dtype=f32, device=dev)
+
+
+def _run(name, *args):
+    """A step that is not timed."""
+    args[-1]()
 
 
 class MoELayer:
@@ -242,6 +268,7 @@ class MoELayer:
       w_dn [G, H, I],                                  w_dn_s [G, H/128, I/128]
     Group E (the last) is the shared expert.
     """
+    CODES = L.QUANT_E4M3   # the experts' operand, as moe_norm writes it
 
     def __init__(self, shape: LayerShape, centroids, bias, w_gu, w_gu_s, w_dn, w_dn_s,
                  gate: Gate | None = None):
@@ -271,21 +298,21 @@ class MoELayer:
 
     @classmethod
     def from_fp32_experts(cls, shape: LayerShape, centroids, bias, gu_fp32, dn_fp32,
-                          device="cuda", gate: Gate | None = None):
+                          device="cuda", gate: Gate | None = None, **kw):
         """Build a layer from per-expert fp32 weights, quantised on the GPU.
 
         gu_fp32 / dn_fp32: iterables of (expert, array [2I, H] / [H, I]) covering
         every group 0..G-1 (G-1 is the shared expert).  Each array is copied
-        to the GPU and quantised there (quantize_into).
+        to the GPU and quantised there (quantize_into).  kw: the class's own.
         """
         w_gu, w_gu_s, w_dn, w_dn_s = cls.empty_weights(shape, device)
         stream = torch.cuda.current_stream()
         for src, q, s in ((gu_fp32, w_gu, w_gu_s), (dn_fp32, w_dn, w_dn_s)):
             for e, arr in src:
                 t = torch.from_numpy(arr).to(device)
-                cls.quantize_into(t[None], q[e:e + 1], s[e:e + 1], stream)
+                cls.quantize_into(t[None], q[e:e + 1], None if s is None else s[e:e + 1], stream)
                 stream.synchronize()
-        return cls(shape, centroids, bias, w_gu, w_gu_s, w_dn, w_dn_s, gate)
+        return cls(shape, centroids, bias, w_gu, w_gu_s, w_dn, w_dn_s, gate, **kw)
 
     def buffers(self, T: int) -> Buffers:
         b = self._bufs.get(T)
@@ -320,8 +347,6 @@ class MoELayer:
         s = self.shape
         T = x_bf16.shape[0]
         b = bufs or self.buffers(T)
-        R = b.R
-        b.gu_kept = keep_gu
         st = stream if stream is not None else torch.cuda.current_stream()
         if self._side is None:
             self._side = torch.cuda.Stream(device=st.device)
@@ -340,14 +365,34 @@ class MoELayer:
             events.setdefault(name, []).append((e0, e1))
 
         side.wait_stream(st)
-        step("quant", side, lambda: L.fp8_quant_1x128(x_bf16, T, s.H, s.H, 0, b.xq, b.xs, side))
+        step("quant", side, lambda: self._quantise(x_bf16, b, side))
         step("route", st, lambda: self._route(x_bf16, b, seq_len, st))
         if seq_len is not None:
             step("seq_balance", st, lambda: self._seq_balance(b, seq_len, alpha, st))
-        step("permute", st, lambda: L.moe_permute(
-            b.topk_idx, b.counts, T, s.k, s.E, s.n_shared, b.offsets, b.perm_src, b.inv_perm,
-            None, None, s.H, None, None, b.perm_ws, b.perm_ws_bytes, st))
+        step("permute", st, lambda: self._permute(b, st))
         st.wait_stream(side)
+        self._experts(x_bf16, b, keep_gu, st, step)
+        shared = b.d[T * s.k:T * s.k + T] if s.n_shared else None
+        step("combine", st, lambda: L.moe_combine(b.d, b.inv_perm, b.topk_w, shared, T, s.k,
+                                                  s.H, b.y, st))
+        if update_bias:
+            step("bias", st, lambda: L.moe_bias_update(b.counts, self.bias, s.E, gamma, st))
+        return b.y
+
+    def _quantise(self, x_bf16, b, stream):
+        """The experts' operand of x."""
+        H = self.shape.H
+        L.fp8_quant_1x128(x_bf16, x_bf16.shape[0], H, H, 0, b.xq, b.xs, stream)
+
+    def _permute(self, b, st):
+        s = self.shape
+        L.moe_permute(b.topk_idx, b.counts, b.T, s.k, s.E, s.n_shared, b.offsets, b.perm_src, b.inv_perm,
+                      None, None, s.H, None, None, b.perm_ws, b.perm_ws_bytes, st)
+
+    def _experts(self, x_bf16, b, keep_gu, st, step):
+        """The experts' rows b.d of the operand and the permutation in b."""
+        s, R = self.shape, b.R
+        b.gu_kept = keep_gu
         if keep_gu:
             step("gate_up", st, lambda: L.grouped_fp8_gemm_swiglu_keep(
                 b.xq, b.xs, b.perm_src, self.w_gu, self.w_gu_s, b.offsets, s.G, R, s.I, s.H,
@@ -358,12 +403,6 @@ class MoELayer:
                 b.hq, b.hs, st))
         step("down", st, lambda: L.grouped_fp8_gemm(
             b.hq, b.hs, None, self.w_dn, self.w_dn_s, b.offsets, s.G, R, s.H, s.I, b.d, st))
-        shared = b.d[T * s.k:T * s.k + T] if s.n_shared else None
-        step("combine", st, lambda: L.moe_combine(b.d, b.inv_perm, b.topk_w, shared, T, s.k,
-                                                  s.H, b.y, st))
-        if update_bias:
-            step("bias", st, lambda: L.moe_bias_update(b.counts, self.bias, s.E, gamma, st))
-        return b.y
 
     def requantize_from_fp32(self, gu_fp32, dn_fp32, stream=None):
         """Requantise both weight sets in place from fp32 master weights
@@ -416,16 +455,13 @@ class MoELayer:
         `events` as in forward, keys "combine_bwd", "dgrad_down",
         "recompute_gate_up", "swiglu_bwd", "dgrad_gate_up", "unpermute",
         "wgrad_down", "wgrad_gate_up", "router_bwd"."""
-        self._check_gate(seq_len)
-        if self.gate is not None and self.shape.E % 16:
-            raise ValueError(f"the backward of a layer with a Gate needs E % 16 == 0, E is {self.shape.E}")
+        self._check_backward(seq_len)
         s = self.shape
         T = dy_bf16.shape[0]
         b = bufs or self.buffers(T)
         bb = bwd or self.backward_buffers(T)
         if keep_intermediates:
             bb.intermediates()
-        R, G, H, I, k, cap = b.R, s.G, s.H, s.I, s.k, bb.cap
         st = stream if stream is not None else torch.cuda.current_stream()
 
         def step(name, fn):
@@ -442,8 +478,17 @@ class MoELayer:
         # the combine and SwiGLU backward also write the 1x128 quantisation of
         # their bf16 gradients (the input-gradient GEMMs' operands)
         step("combine_bwd", lambda: L.moe_combine_backward(
-            dy_bf16, b.inv_perm, b.topk_w, b.d, T, k, H, s.n_shared, bb.dD, bb.dw, st,
+            dy_bf16, b.inv_perm, b.topk_w, b.d, T, s.k, s.H, s.n_shared, bb.dD, bb.dw, st,
             d_expert_out_e4m3=bb.dDq, d_expert_out_scale=bb.dDs))
+        self._experts_backward(x_bf16, b, bb, keep_intermediates, st, step)
+        self._router_backward(x_bf16, b, bb, seq_len, alpha, st, step)
+        return bb
+
+    def _experts_backward(self, x_bf16, b, bb, keep_intermediates, st, step):
+        """From the gradient of the experts' rows in bb to their input's (bb.dx)
+        and the weights'."""
+        s, T = self.shape, b.T
+        R, G, H, I, k, cap = b.R, s.G, s.H, s.I, s.k, bb.cap
         step("dgrad_down", lambda: L.grouped_fp8_gemm_dgrad(
             bb.dDq, bb.dDs, self.w_dn, self.w_dn_s, b.offsets, G, R, H, I, bb.dh, st))
         if getattr(b, "gu_kept", False):
@@ -461,9 +506,7 @@ class MoELayer:
             bb.s_dgu, bb.c_h, bb.s_h, st))
         step("dgrad_gate_up", lambda: L.grouped_fp8_gemm_dgrad(
             bb.dguq, bb.dgus, self.w_gu, self.w_gu_s, b.offsets, G, R, 2 * I, H, bb.dxp, st))
-        shared = bb.dxp[T * k:T * k + T] if s.n_shared else None
-        step("unpermute", lambda: L.moe_combine(bb.dxp, b.inv_perm, bb.ones, shared, T, k, H,
-                                                bb.dx, st))
+        step("unpermute", lambda: self._unpermute(b, bb, st))
         step("wgrad_down", lambda: (
             L.fp8_quant_128x1_grouped(bb.dD, H, None, b.offsets, G, R, H, bb.c_dD, bb.s_dD, cap, st),
             L.grouped_fp8_wgrad(bb.c_dD, bb.s_dD, bb.c_h, bb.s_h, cap, b.offsets, G, R, H, I,
@@ -473,6 +516,16 @@ class MoELayer:
                                       cap, st),
             L.grouped_fp8_wgrad(bb.c_dgu, bb.s_dgu, bb.c_x, bb.s_x, cap, b.offsets, G, R, 2 * I, H,
                                 bb.dW_gu, st)))
+
+    def _unpermute(self, b, bb, st):
+        s, T = self.shape, b.T
+        shared = bb.dxp[T * s.k:T * s.k + T] if s.n_shared else None
+        L.moe_combine(bb.dxp, b.inv_perm, bb.ones, shared, T, s.k, s.H, bb.dx, st)
+
+    def _router_backward(self, x_bf16, b, bb, seq_len, alpha, st, step):
+        """The router's part on top of bb.dx: bb.dx_total and bb.dC."""
+        s, T = self.shape, b.T
+        H, k = s.H, s.k
         if self.gate is not None:
             g = self.gate
             bb.dense()
@@ -497,7 +550,11 @@ class MoELayer:
                 x_bf16, self.centroids, b.topk_idx, bb.dw, b.scores, b.score_sums, b.seq_f, T, H,
                 s.E, k, seq_len, alpha, bb.dx, bb.dx_total, bb.dC, bb.dlogit, bb.dense_ws,
                 bb.dense_ws_bytes, st))
-        return bb
+
+    def _check_backward(self, seq_len):
+        self._check_gate(seq_len)
+        if self.gate is not None and self.shape.E % 16:
+            raise ValueError(f"the backward of a layer with a Gate needs E % 16 == 0, E is {self.shape.E}")
 
     def _check_gate(self, seq_len):
         """What a layer with a Gate does not do, before anything is launched."""
@@ -551,6 +608,7 @@ class Int8MoELayer(MoELayer):
       w_dn [G, H, I],                                       w_dn_s [G, H]
     Built by from_fp32_experts like MoELayer; inference only.
     """
+    CODES = L.QUANT_INT8
 
     @staticmethod
     def empty_weights(shape: LayerShape, device="cuda"):
@@ -579,27 +637,33 @@ class Int8MoELayer(MoELayer):
         s = self.shape
         T = x_bf16.shape[0]
         b = bufs or self.buffers(T)
-        R = b.R
         st = stream if stream is not None else torch.cuda.current_stream()
         if self._side is None:
             self._side = torch.cuda.Stream(device=st.device)
         side = self._side
         side.wait_stream(st)
-        L.int8_quant_rows(x_bf16, T, s.H, s.H, b.xq, b.xs, side)
+        self._quantise(x_bf16, b, side)
         self._route(x_bf16, b, None, st)
-        L.moe_permute(b.topk_idx, b.counts, T, s.k, s.E, s.n_shared, b.offsets, b.perm_src,
-                      b.inv_perm, None, None, s.H, None, None, b.perm_ws, b.perm_ws_bytes, st)
+        self._permute(b, st)
         st.wait_stream(side)
-        L.grouped_int8_gemm_swiglu(b.xq, b.xs, b.perm_src, self.w_gu, self.w_gu_s, b.offsets, s.G,
-                                   R, s.I, s.H, b.h, st)
-        L.int8_quant_rows(b.h, R, s.I, s.I, b.hq, b.hs, st)
-        L.grouped_int8_gemm(b.hq, b.hs, None, self.w_dn, self.w_dn_s, b.offsets, s.G, R, s.H, s.I,
-                            b.d, st)
+        self._experts(x_bf16, b, False, st, _run)
         shared = b.d[T * s.k:T * s.k + T] if s.n_shared else None
         L.moe_combine(b.d, b.inv_perm, b.topk_w, shared, T, s.k, s.H, b.y, st)
         if update_bias:
             L.moe_bias_update(b.counts, self.bias, s.E, gamma, st)
         return b.y
+
+    def _quantise(self, x_bf16, b, stream):
+        H = self.shape.H
+        L.int8_quant_rows(x_bf16, x_bf16.shape[0], H, H, b.xq, b.xs, stream)
+
+    def _experts(self, x_bf16, b, keep_gu, st, step):
+        s, R = self.shape, b.R
+        L.grouped_int8_gemm_swiglu(b.xq, b.xs, b.perm_src, self.w_gu, self.w_gu_s, b.offsets, s.G,
+                                   R, s.I, s.H, b.h, st)
+        L.int8_quant_rows(b.h, R, s.I, s.I, b.hq, b.hs, st)
+        L.grouped_int8_gemm(b.hq, b.hs, None, self.w_dn, self.w_dn_s, b.offsets, s.G, R, s.H, s.I,
+                            b.d, st)
 
     def requantize_from_fp32(self, gu_fp32, dn_fp32, stream=None):
         """Requantise both weight sets in place from fp32 weights ([G, 2I, H]
@@ -609,3 +673,238 @@ class Int8MoELayer(MoELayer):
 
     def backward(self, *args, **kw):
         raise NotImplementedError("Int8MoELayer is a forward only: train with MoELayer")
+
+
+class Bf16Buffers(Buffers):
+    """Device buffers of one bf16 forward at T tokens (reused across calls)."""
+
+    def _operands(self):
+        """h in bf16 (x is read as it is)."""
+        self.h = torch.empty((self.R, self._shape.I), dtype=torch.bfloat16, device=self._dev)
+
+
+class Bf16BackwardBuffers(BackwardBuffers):
+    """Device buffers of one bf16 layer backward at T tokens (reused across calls)."""
+
+    def _operands(self):
+        self.dgu = torch.empty((self.R, 2 * self._shape.I), dtype=torch.bfloat16, device=self._dev)
+        self.dDq = self.dDs = self._gu = None
+
+    @property
+    def gu(self):
+        """Gate and up outputs formed again, after a forward that kept none
+        (allocated on first use)."""
+        if self._gu is None:
+            self._gu = torch.empty_like(self.dgu)
+        return self._gu
+
+
+class Bf16MoELayer(MoELayer):
+    """The layer with its expert weights and activations in bf16, forward and
+    backward: for training or checking without quantisation.
+
+      w_gu [G, 2I, H] bf16 (rows [0, I) gate, [I, 2I) up), w_dn [G, H, I]
+    act: the gate's activation, ACT_SILU or ACT_GELU.  Built by
+    from_fp32_experts like MoELayer (the fp32 weights are rounded to bf16).
+    """
+    CODES = L.QUANT_NONE
+
+    def __init__(self, shape: LayerShape, centroids, bias, w_gu, w_gu_s, w_dn, w_dn_s,
+                 gate: Gate | None = None, act: int = L.ACT_SILU):
+        super().__init__(shape, centroids, bias, w_gu, w_gu_s, w_dn, w_dn_s, gate)
+        self.act = act
+
+    @staticmethod
+    def empty_weights(shape: LayerShape, device="cuda"):
+        """w_gu, None, w_dn, None: bf16 weights have no scales."""
+        s, dev = shape, torch.device(device)
+        return (torch.empty((s.G, 2 * s.I, s.H), dtype=torch.bfloat16, device=dev), None,
+                torch.empty((s.G, s.H, s.I), dtype=torch.bfloat16, device=dev), None)
+
+    @staticmethod
+    def quantize_into(w_f32, out_q, out_s=None, stream=None):
+        """fp32 weights rounded to bf16."""
+        st = stream if stream is not None else torch.cuda.current_stream()
+        with torch.cuda.stream(st):
+            out_q.copy_(w_f32)
+
+    def buffers(self, T: int) -> Bf16Buffers:
+        b = self._bufs.get(T)
+        if b is None:
+            b = self._bufs[T] = Bf16Buffers(self.shape, T, self.centroids.device)
+        return b
+
+    def backward_buffers(self, T: int) -> Bf16BackwardBuffers:
+        bb = self._bwd.get(T)
+        if bb is None:
+            bb = self._bwd[T] = Bf16BackwardBuffers(self.shape, T, self.centroids.device)
+        return bb
+
+    def requantize_from_fp32(self, gu_fp32, dn_fp32, stream=None):
+        """Both weight sets in place from fp32 master weights ([G, 2I, H] and
+        [G, H, I] device tensors), rounded to bf16."""
+        self.quantize_into(gu_fp32, self.w_gu, None, stream)
+        self.quantize_into(dn_fp32, self.w_dn, None, stream)
+
+    def _quantise(self, x_bf16, b, stream):
+        pass
+
+    def _experts(self, x_bf16, b, keep_gu, st, step):
+        s, R = self.shape, b.R
+        b.gu_kept = keep_gu
+        step("gate_up", st, lambda: L.grouped_bf16_gemm_glu(
+            x_bf16, b.perm_src, self.w_gu, b.offsets, s.G, R, s.I, s.H, self.act, b.h,
+            b.hgu if keep_gu else None, st))
+        step("down", st, lambda: L.grouped_bf16_gemm(b.h, None, self.w_dn, b.offsets, s.G, R, s.H, s.I, b.d,
+                                                     st))
+
+    def _experts_backward(self, x_bf16, b, bb, keep_intermediates, st, step):
+        s = self.shape
+        R, G, H, I = b.R, s.G, s.H, s.I
+        if getattr(b, "gu_kept", False):
+            gu = b.hgu
+        else:
+            gu = bb.gu
+            step("recompute_gate_up", lambda: L.grouped_bf16_gemm(
+                x_bf16, b.perm_src, self.w_gu, b.offsets, G, R, 2 * I, H, gu, st))
+        # the down projection's input gradient and the activation's backward
+        step("dgrad_down", lambda: L.grouped_bf16_gemm_dgrad_glu(
+            bb.dD, self.w_dn, gu, b.offsets, G, R, H, I, self.act, bb.dgu, st))
+        step("dgrad_gate_up", lambda: L.grouped_bf16_gemm_dgrad(
+            bb.dgu, self.w_gu, b.offsets, G, R, 2 * I, H, bb.dxp, st))
+        step("unpermute", lambda: self._unpermute(b, bb, st))
+        step("wgrad_down", lambda: L.grouped_bf16_wgrad(
+            bb.dD, b.h, None, b.offsets, G, R, H, I, bb.dW_dn, st))
+        step("wgrad_gate_up", lambda: L.grouped_bf16_wgrad(
+            bb.dgu, x_bf16, b.perm_src, b.offsets, G, R, 2 * I, H, bb.dW_gu, st))
+
+
+class BlockBuffers:
+    """Device buffers of a MoEBlock at T tokens of the residual stream's type
+    (reused across calls)."""
+
+    def __init__(self, shape: LayerShape, T: int, dtype, device="cuda"):
+        dev, f32 = torch.device(device), torch.float32
+        self.T, self.H, self.dtype, self._dev = T, shape.H, dtype, dev
+        self.n = torch.empty((T, shape.H), dtype=torch.bfloat16, device=dev)
+        self.rstd = torch.empty((T,), dtype=f32, device=dev)
+        self.y = torch.empty((T, shape.H), dtype=dtype, device=dev)
+        self.added = False
+        self._sum = self.dx = None
+
+    @property
+    def sum(self):
+        """The residual stream after a forward's add (allocated on first use)."""
+        if self._sum is None:
+            self._sum = torch.empty_like(self.y)
+        return self._sum
+
+    def gradients(self):
+        """Buffers of the backward (allocated on first use): dx [T, H],
+        d_weight, d_post_weight [H], d_shared_w [T] and the workspace."""
+        if self.dx is None:
+            dev, f32 = self._dev, torch.float32
+            self.dx = torch.empty_like(self.y)
+            self.d_weight = torch.empty((self.H,), dtype=f32, device=dev)
+            self.d_post_weight = torch.empty((self.H,), dtype=f32, device=dev)
+            self.d_shared_w = torch.empty((self.T,), dtype=f32, device=dev)
+            self.ws_bytes = max(L.moe_norm_backward_workspace_bytes(self.T, self.H),
+                                L.moe_combine_norm_backward_workspace_bytes(self.T, self.H))
+            self.ws = torch.empty((max(16, self.ws_bytes),), dtype=torch.uint8, device=dev)
+        return self
+
+
+class MoEBlock:
+    """A layer between its norms, on the residual stream (bf16 or fp32):
+
+      v = x + add (or x);  n = norm(v) * weight
+      y = residual_scale * v + scale * [norm](layer(n)) * post_weight
+
+    moe_norm writes the experts' operand beside n, and moe_combine_norm takes
+    the layer's combine with the norm after it and the residual sum, so neither
+    is a pass of its own.  layer: a MoELayer, Bf16MoELayer or Int8MoELayer.
+    post_norm: norm the layer's output; without it post_weight (optional)
+    scales its channels.  Weights are fp32 [H]."""
+
+    def __init__(self, layer: MoELayer, weight=None, eps: float = 1e-6, post_norm: bool = False,
+                 post_weight=None, residual_scale: float = 1.0, scale: float = 1.0):
+        self.layer, self.weight, self.eps = layer, weight, eps
+        self.post_norm, self.post_weight = post_norm, post_weight
+        self.residual_scale, self.scale = residual_scale, scale
+        self._bufs = {}
+
+    def buffers(self, T: int, dtype) -> BlockBuffers:
+        key = (T, dtype)
+        if key not in self._bufs:
+            self._bufs[key] = BlockBuffers(self.layer.shape, T, dtype, self.layer.centroids.device)
+        return self._bufs[key]
+
+    def forward(self, x, add=None, shared_w=None, stream=None, update_bias: bool = False,
+                gamma: float = 0.001, seq_len: int | None = None, alpha: float = 0.0001,
+                keep_gu: bool = False) -> torch.Tensor:
+        """One block forward of x [T, H] (fp32 or bf16), with add [T, H] bf16
+        added to the stream first.  shared_w [T] fp32: the shared expert's own
+        gate.  The rest as in the layer's forward.  Returns y in the buffers of
+        this T and type (buffers(T, x.dtype).sum holds v after an add)."""
+        layer, s = self.layer, self.layer.shape
+        layer._check_gate(seq_len)
+        T = x.shape[0]
+        f, b = self.buffers(T, x.dtype), layer.buffers(T)
+        st = stream if stream is not None else torch.cuda.current_stream()
+        f.added = add is not None
+        v = f.sum if f.added else x
+        codes, scales = (None, None) if layer.CODES == L.QUANT_NONE else (b.xq, b.xs)
+        L.moe_norm(x, add, self.weight, T, s.H, self.eps, v if f.added else None, f.n, f.rstd, layer.CODES,
+                   codes, scales, st)
+        layer._route(f.n, b, seq_len, st)
+        if seq_len is not None:
+            layer._seq_balance(b, seq_len, alpha, st)
+        layer._permute(b, st)
+        layer._experts(f.n, b, keep_gu, st, _run)
+        shared = b.d[T * s.k:T * s.k + T] if s.n_shared else None
+        L.moe_combine_norm(b.d, b.inv_perm, b.topk_w, shared, shared_w, v, self.residual_scale, self.post_norm,
+                           self.post_weight, self.eps, self.scale, T, s.k, s.H, f.y, None, st)
+        if update_bias:
+            L.moe_bias_update(b.counts, layer.bias, s.E, gamma, st)
+        return f.y
+
+    def backward(self, dy, x, shared_w=None, stream=None, seq_len: int | None = None,
+                 alpha: float = 0.0001):
+        """Backward for the output gradient dy (x's type) after a forward of x
+        (with the same shared_w and seq_len).  Returns (the block's buffers, the
+        layer's backward buffers): dx - the gradient of x and of add alike -,
+        d_weight, d_post_weight (with a post_norm or post_weight) and d_shared_w
+        (with shared_w); dC, dW_gu, dW_dn, dw of the layer."""
+        layer, s = self.layer, self.layer.shape
+        if isinstance(layer, Int8MoELayer):
+            layer.backward()
+        layer._check_backward(seq_len)
+        if dy.dtype != x.dtype or dy.shape != x.shape:
+            raise ValueError(f"dy {tuple(dy.shape)} {dy.dtype} and x {tuple(x.shape)} {x.dtype} differ")
+        T = dy.shape[0]
+        f, b, bb = self.buffers(T, dy.dtype).gradients(), layer.buffers(T), layer.backward_buffers(T)
+        st = stream if stream is not None else torch.cuda.current_stream()
+        weighted = self.post_weight is not None
+        L.moe_combine_norm_backward(
+            dy, b.inv_perm, b.topk_w, b.d, s.n_shared, shared_w, self.post_norm, self.post_weight, self.eps,
+            self.scale, T, s.k, s.H, bb.dD, bb.dw, f.d_shared_w if shared_w is not None else None, bb.dDq, bb.dDs,
+            f.d_post_weight if weighted else None, f.ws, f.ws_bytes, st)
+        layer._experts_backward(f.n, b, bb, False, st, _run)
+        layer._router_backward(f.n, b, bb, seq_len, alpha, st, _run)
+        L.moe_norm_backward(bb.dx_total, f.sum if f.added else x, self.weight, f.rstd, dy, self.residual_scale, T,
+                            s.H, f.dx, f.d_weight if self.weight is not None else None, f.ws, f.ws_bytes, st)
+        return f, bb
+
+    def capture(self, x, add=None, **forward_kw):
+        """One forward captured as a HIP graph on the buffers of this T and type,
+        as MoELayer.capture."""
+        side = torch.cuda.Stream()   # default priority
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            self.forward(x, add, stream=side, **forward_kw)   # warm-up outside the capture
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            self.forward(x, add, stream=torch.cuda.current_stream(), **forward_kw)
+        return graph
