@@ -32,9 +32,9 @@ FLAGS = [
     "-mllvm", "-amdgpu-mfma-vgpr-form",
     "-I", INCLUDE, "-I", CSRC,
 ]
-# the int8 tile kernel keeps its accumulators in AGPRs: one wave a SIMD with
-# all 512 registers
-AGPR_FORM = {"int8_wide.hip"}
+# the wide int8 and bf16 tile kernels keep their accumulators in AGPRs: one wave
+# a SIMD with all 512 registers
+AGPR_FORM = {"int8_wide.hip", "bf16_wide.hip"}
 
 
 def flags(src):

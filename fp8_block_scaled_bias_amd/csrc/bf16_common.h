@@ -110,6 +110,9 @@ __device__ __forceinline__ v4i tr_read(const uint8_t* tile, uint32_t lane_off, i
 
 void launch_zero(float* p, int64_t n, hipStream_t st);  // n a multiple of 4
 
+// 256 x 256 tiles (bf16_wide.hip).  Requires, with an index, A_rows * K < 2^31.
+void launch_wide(const Args& a, Mode m, hipStream_t st);
+
 // 128 x 128 tiles (bf16_mid.hip): any size.
 void launch_mid(const Args& a, Mode m, hipStream_t st);
 

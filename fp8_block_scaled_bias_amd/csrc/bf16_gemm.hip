@@ -41,7 +41,9 @@ int run(const char* who, Mode m, const Args& a, const char* n_name, const char* 
               "%s: operands must be 16-byte aligned, indices 4-byte", who);
   MOE_INVALID(a.out != a.P && a.out != a.Q && a.out != a.gu_in && (!a.keep || a.keep != a.out),
               "%s: outputs must not alias inputs or each other", who);
-  launch_mid(a, m, st);
+  const Plan p = plan(Shape{m, a.index != nullptr, a.A_rows, a.G, a.M_total, a.N, a.K}, gemm::num_cus());
+  if (p == kWide) launch_wide(a, m, st);
+  else launch_mid(a, m, st);
   return check_launch(who);
 }
 
