@@ -113,6 +113,9 @@ void launch_zero(float* p, int64_t n, hipStream_t st);  // n a multiple of 4
 // 256 x 256 tiles (bf16_wide.hip).  Requires, with an index, A_rows * K < 2^31.
 void launch_wide(const Args& a, Mode m, hipStream_t st);
 
+// The weights straight into registers (bf16_stream.hip): kPlain and kGlu, any size.
+void launch_stream(const Args& a, Mode m, Plan p, hipStream_t st);
+
 // 128 x 128 tiles (bf16_mid.hip): any size.
 void launch_mid(const Args& a, Mode m, hipStream_t st);
 

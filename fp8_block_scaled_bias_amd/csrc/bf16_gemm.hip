@@ -43,7 +43,8 @@ int run(const char* who, Mode m, const Args& a, const char* n_name, const char* 
               "%s: outputs must not alias inputs or each other", who);
   const Plan p = plan(Shape{m, a.index != nullptr, a.A_rows, a.G, a.M_total, a.N, a.K}, gemm::num_cus());
   if (p == kWide) launch_wide(a, m, st);
-  else launch_mid(a, m, st);
+  else if (p == kMid) launch_mid(a, m, st);
+  else launch_stream(a, m, p, st);
   return check_launch(who);
 }
 

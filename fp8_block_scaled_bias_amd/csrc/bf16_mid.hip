@@ -2,8 +2,10 @@
 // v_mfma_f32_32x32x16_bf16, every mode and size.
 //
 // A K block of 64 values of both operands (32 KB) goes through a ring of four
-// stages in LDS, three of them on their way (copies straight into LDS), on
-// across a workgroup's tiles; one barrier a K block.  An operand whose
+// stages in LDS (copies straight into LDS), on across a workgroup's tiles, and
+// from there into registers a block before it is multiplied, so that its stage
+// is free for the block four further: three are on their way.  One barrier a K
+// block.  An operand whose
 // contraction runs along its rows lies in 128 rows of 128 B, one whose
 // contraction runs down its rows (the weights of an input gradient, both
 // operands of a weight gradient) in 64 rows of 256 B, and is read transposed.
@@ -44,6 +46,7 @@ __global__ __launch_bounds__(MT, 1) void mid_kernel(Args a) {
   __shared__ int s_pref[MAXG + 1];
   __shared__ int s_red[4];
   __shared__ int s_carry;
+  __shared__ int s_idx[PT ? 4 * 4 * 64 : 1];  // kWgrad: a wave's row indices of four K blocks
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wv >> 1, wn = wv & 1, q = lane >> 5, l32 = lane & 31;
@@ -98,48 +101,83 @@ __global__ __launch_bounds__(MT, 1) void mid_kernel(Args a) {
   int co = 0, ck = 0;
   uint32_t cs = 0;
   Place cp = place(0);
+  // A lane's places in the K block to be copied; they move by a block's bytes.
   const uint8_t* pp[COPIES];
   const uint8_t* pq[COPIES];
+  const int64_t step_p = PT ? 128 * a.N : 128, step_q = QT ? 128 * a.K : 128;
   auto aim = [&]() {
     const int64_t cols = min<int64_t>(TN, NC - cp.n0);
+    const int64_t k0 = PT ? min<int64_t>(s_offs[cp.g], a.M_total - 1) : 0;
 #pragma unroll
     for (int c = 0; c < COPIES; ++c) {
-      const int row = 32 * wv + 8 * c + (lane >> 3);
+      const int row = 32 * wv + 8 * c + (lane >> 3), along = 8 * ((lane & 7) ^ swz(row));
       const int krow = 16 * wv + 4 * c + (lane >> 4), chunk = (lane & 15) ^ (4 * (krow & 3));
       if (PT)
-        pp[c] = reinterpret_cast<const uint8_t*>(a.P + cp.m0 + min(8 * chunk, cp.rows - 8));
+        pp[c] = reinterpret_cast<const uint8_t*>(a.P + (k0 + krow) * a.N + cp.m0 + min(8 * chunk, cp.rows - 8));
       else
         pp[c] = reinterpret_cast<const uint8_t*>(
-            a.P + source((int64_t)cp.m0 + min(row, cp.rows - 1)) * (QT ? a.N : a.K));
+            a.P + source((int64_t)cp.m0 + min(row, cp.rows - 1)) * (QT ? a.N : a.K) + along);
       if (QT) {
-        const int64_t at = PT ? 0 : (int64_t)cp.g * q_rows * a.K;
-        pq[c] = reinterpret_cast<const uint8_t*>(a.Q + at + cp.n0 + min<int64_t>(8 * chunk, cols - 8));
+        // (gathered rows: from the indices, block by block)
+        const int64_t at = PT ? (a.index ? 0 : k0 + krow) : (int64_t)cp.g * q_rows + krow;
+        pq[c] = reinterpret_cast<const uint8_t*>(a.Q + at * a.K + cp.n0 + min<int64_t>(8 * chunk, cols - 8));
       } else {
         const int64_t col = GLU ? (row & (TN - 1)) : row;
         const int64_t at = (int64_t)cp.g * q_rows + (GLU && row >= TN ? a.N : 0) + cp.n0 + min(col, cols - 1);
-        pq[c] = reinterpret_cast<const uint8_t*>(a.Q + at * a.K);
+        pq[c] = reinterpret_cast<const uint8_t*>(a.Q + at * a.K + along);
       }
     }
   };
-  auto copy_block = [&]() {
-    const uint32_t m = lds0 + cs * STAGE + (uint32_t)wv * 4096;
-#pragma unroll
-    for (int c = 0; c < COPIES; ++c) {
-      const int row = 32 * wv + 8 * c + (lane >> 3);
-      const int along = min(64 * ck + 8 * ((lane & 7) ^ swz(row)), cp.kc - 8) * 2;
-      const int krow = 16 * wv + 4 * c + (lane >> 4);
-      // (of a group without rows: a row of another, or the first one)
-      int64_t down = max(0, min(64 * ck + krow, cp.kc - 1));
-      if (PT) down = min<int64_t>(s_offs[cp.g] + down, a.M_total - 1);
-      dma16(PT ? pp[c] + down * a.N * 2 : pp[c] + along, m + c * 1024);
-      dma16(QT ? pq[c] + (PT ? source(down) : down) * a.K * 2 : pq[c] + along, m + REG + c * 1024);
+  // kWgrad's indices are copied three blocks ahead of the copies that use them
+  int xo = 0, xk = 0, xb = 0, cb = 0;
+  Place xp = cp;
+  auto index_block = [&]() {
+    const int64_t row = min<int64_t>((int64_t)s_offs[xp.g] + 64 * xk + lane, a.M_total - 1);
+    gemm::dma4(a.index + row, (uint32_t)(uintptr_t)s_idx + (uint32_t)((wv * 4 + (xb & 3)) * 256));
+    ++xb;
+    if (++xk == xp.nkb) {
+      xk = 0;
+      xp = place(++xo);
     }
+  };
+  // copies 2 N and 2 N + 1 of a K block's eight
+  uint32_t m_copy = 0;
+  int c_left = 0;
+  auto copy_begin = [&]() __attribute__((always_inline)) {
+    if (PT && a.index) index_block();
+    m_copy = lds0 + cs * STAGE + (uint32_t)wv * 4096;
+    c_left = max(1, cp.kc - 64 * ck);
+  };
+  auto copy_pair = [&](int c) __attribute__((always_inline)) {
+    const uint8_t *p = pp[c], *w = pq[c];
+    const int krow = 16 * wv + 4 * c + (lane >> 4);
+    if (PT && a.index)
+      w += (int64_t)min((uint32_t)s_idx[(wv * 4 + (cb & 3)) * 64 + krow], (uint32_t)(a.A_rows - 1)) * (2 * a.K);
+    if (c_left < 64) {  // what lies past the end: the last values again
+      const int row = 32 * wv + 8 * c + (lane >> 3);
+      const int along = max(0, 8 * ((lane & 7) ^ swz(row)) - (c_left - 8)) * 2, down = max(0, krow - (c_left - 1));
+      p -= PT ? down * (2 * a.N) : along;
+      if (!(PT && a.index)) w -= QT ? down * (2 * a.K) : along;
+    }
+    dma16(p, m_copy + c * 1024);
+    dma16(w, m_copy + REG + c * 1024);
+    pp[c] += step_p;
+    if (!(PT && a.index)) pq[c] += step_q;
+  };
+  auto copy_end = [&]() __attribute__((always_inline)) {
+    ++cb;
     cs = cs + 1 == S ? 0 : cs + 1;
     if (++ck == cp.nkb) {
       ck = 0;
       cp = place(++co);
       aim();
     }
+  };
+  auto copy_block = [&]() {
+    copy_begin();
+#pragma unroll
+    for (int c = 0; c < COPIES; ++c) copy_pair(c);
+    copy_end();
   };
 
   uint32_t o[4];  // lane (q, l32): chunk 2 ks + q of row l32 of a 32-row block
@@ -200,46 +238,64 @@ __global__ __launch_bounds__(MT, 1) void mid_kernel(Args a) {
     }
   };
 
+  if (PT && a.index) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) index_block();
+    wait_copies<0>();
+  }
   aim();
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) copy_block();
+  for (int s = 0; s < S; ++s) {
+    copy_block();
+    if (PT && a.index) wait_copies<0>();  // (the first blocks' indices are not so far ahead)
+  }
+  v4i fp[2][2][4], fq[2][2][4];  // operands: [block in turn][32 rows][ks]
+  uint32_t st = 0;
+  auto read_ks = [&](v4i (&xp)[2][4], v4i (&xq)[2][4], int ks) __attribute__((always_inline)) {
+    const uint8_t* tp = smem + st * STAGE;
+    const uint8_t* tq = tp + REG;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      xq[i][ks] = QT ? tr_read(tq, otr, wn + 2 * i, ks)
+                     : *reinterpret_cast<const v4i*>(tq + o[ks] + (32 * wn + 64 * i) * 128);
+      xp[i][ks] = PT ? tr_read(tp, otr, wm + 2 * i, ks)
+                     : *reinterpret_cast<const v4i*>(tp + o[ks] + (32 * wm + 64 * i) * 128);
+    }
+  };
+  wait_copies<(S - 1) * 2 * COPIES>();
+  barrier();
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) read_ks(fp[0], fq[0], ks);
+  st = 1;
   clear();
   int t_o = 0, t_k = 0;
   Place p = place(0);
-  uint32_t st = 0;
-  while (t_o < my_n) {
-    // this block's copies have landed (those of S - 2 blocks come after them),
-    // and everyone is past the block whose stage is filled next
+  auto step = [&](v4i (&xp)[2][4], v4i (&xq)[2][4], v4i (&np)[2][4], v4i (&nq)[2][4]) __attribute__((always_inline)) {
+    // the next block's copies have landed (those of two blocks come after
+    // them), and everyone has this block in registers
     wait_copies<(S - 2) * 2 * COPIES>();
     barrier();
-    copy_block();
-    const uint8_t* tp = smem + st * STAGE;
-    const uint8_t* tq = tp + REG;
-    v4i fp[2][4], fq[2][4];
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        fq[i][ks] = QT ? tr_read(tq, otr, wn + 2 * i, ks)
-                       : *reinterpret_cast<const v4i*>(tq + o[ks] + (32 * wn + 64 * i) * 128);
-        fp[i][ks] = PT ? tr_read(tp, otr, wm + 2 * i, ks)
-                       : *reinterpret_cast<const v4i*>(tp + o[ks] + (32 * wm + 64 * i) * 128);
-      }
     const int left = p.kc - 64 * t_k;
     if (left < 64)
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          fq[i][ks] = keep_first(fq[i][ks], left - 16 * ks - 8 * q);
-          fp[i][ks] = keep_first(fp[i][ks], left - 16 * ks - 8 * q);
+          xq[i][ks] = keep_first(xq[i][ks], left - 16 * ks - 8 * q);
+          xp[i][ks] = keep_first(xp[i][ks], left - 16 * ks - 8 * q);
         }
+    copy_begin();
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
+    for (int ks = 0; ks < 4; ++ks) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = mfma(fq[j][ks], fp[i][ks], acc[i][j]);
+        for (int j = 0; j < 2; ++j) acc[i][j] = mfma(xq[j][ks], xp[i][ks], acc[i][j]);
+      read_ks(np, nq, ks);
+      copy_pair(ks);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    copy_end();
     st = st + 1 == S ? 0 : st + 1;
     if (++t_k == p.nkb) {
       finish(p);
@@ -247,6 +303,11 @@ __global__ __launch_bounds__(MT, 1) void mid_kernel(Args a) {
       t_k = 0;
       p = place(++t_o);
     }
+  };
+  while (t_o < my_n) {
+    step(fp[0], fq[0], fp[1], fq[1]);
+    if (t_o == my_n) break;
+    step(fp[1], fq[1], fp[0], fq[0]);
   }
   wait_copies<0>();  // what was copied past the last tile lands before the LDS is released
 }

@@ -14,6 +14,13 @@ enum Mode { kPlain = 0, kGlu = 1, kDgrad = 2, kDgradGlu = 3, kWgrad = 4 };
 enum Plan {
   kWide = 0,  // 256 x 256 tiles (bf16_wide.hip)
   kMid = 1,   // 128 x 128 tiles (bf16_mid.hip)
+  // weights into registers (bf16_stream.hip; kPlain and kGlu only): a workgroup
+  // a tile of so many rows and weight rows
+  kSplit16x64 = 2,
+  kSplit16x16 = 3,
+  kSplit64x64 = 4,
+  kSplit64x32 = 5,  // (never with kGlu)
+  kSplit64x16 = 6,
 };
 
 struct Shape {
@@ -25,13 +32,41 @@ struct Shape {
 
 inline int64_t parts(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Row tiles and column tiles of the register kernels (the host does not know
+// the groups' own sizes: at most so many, or what groups of average size have)
+inline int64_t m16(const Shape& s) { return std::min(s.M_total, s.G + s.M_total / 16); }
+inline int64_t m64(const Shape& s) { return s.G * parts(s.M_total / s.G, 64); }
+inline int64_t n64(const Shape& s) { return parts(s.N, s.mode == kGlu ? 32 : 64); }
+inline int64_t n32(const Shape& s) { return parts(s.N, 32); }
+inline int64_t n16(const Shape& s) { return parts(s.N, s.mode == kGlu ? 8 : 16); }
+
+// A 256 x 256 tile takes as long as two of 128 x 128, one a CU, so the wide
+// tiles are taken where they save more than half of the rounds of the CUs.
+// Times (wide / mid), 64 groups, N = 4096, K = 7168: 17 rows 690 / 625 us, 64:
+// 733 / 682, 128: 792 / 778, 256: 908 / 1259; one group: 1024 rows 132 / 71, 2048:
+// 141 / 137, 4096: 187 / 281; the input gradient of one group: 1024 rows 93 / 87,
+// 2048: 107 / 167.
+//
+// The register kernels where there are too few tiles for the CUs: of few rows
+// (16 rows of one group 15 us, 55 with 128 x 128 tiles; four groups 35 and 58,
+// eight 82 and 83) and of up to a 64 x 64 tile a CU (256 rows of one group 54
+// and 57 us).  The widest column tile that gives every CU one: 64 rows of one
+// group 53 us with 64, 40 with 32, 35 with 16 weight rows.
 inline Plan plan(const Shape& s, int64_t cus) {
   const int64_t avg = s.M_total / s.G;
   const int64_t rows = s.mode == kWgrad ? s.N : avg;
   const int64_t cols = s.mode == kPlain ? s.N : s.mode == kGlu ? 2 * s.N : s.K;
-  const int64_t wide_tiles = s.G * parts(rows, 256) * parts(cols, 256);
+  auto rounds = [&](int64_t tile) { return parts(s.G * parts(rows, tile) * parts(cols, tile), cus); };
   const bool fits = !s.gather || s.A_rows * s.K < 0x7FF80000ll;  // 32-bit offsets into a gathered A
-  return fits && wide_tiles >= cus && (s.mode == kWgrad || avg > 16) ? kWide : kMid;
+  const Plan tiles = fits && rounds(128) > 2 * rounds(256) ? kWide : kMid;
+  if (s.mode >= kDgrad) return tiles;
+  if (avg <= 16) {
+    const int64_t n = m16(s) * n64(s);
+    return n >= 2 * cus ? tiles : n >= cus ? kSplit16x64 : kSplit16x16;
+  }
+  if (s.G * parts(avg, 64) * parts(cols, 64) > cus) return tiles;
+  if (m64(s) * n64(s) >= cus) return kSplit64x64;
+  return s.mode != kGlu && m64(s) * n32(s) >= cus ? kSplit64x32 : kSplit64x16;
 }
 
 }  // namespace bf16
