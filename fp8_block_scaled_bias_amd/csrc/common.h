@@ -88,6 +88,21 @@ __device__ __forceinline__ float quad_lane3(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0xFF, 0xF, 0xF, true));
 }
 
+// The value of the lane 1, 2, 4, 8 away in a row of 16, where the lanes nearer
+// than that already agree (DPP: quad_perm, row_half_mirror, row_mirror).
+template <int D>
+__device__ __forceinline__ float row_other(float v) {
+  constexpr int ctrl = D == 1 ? 0xB1 : D == 2 ? 0x4E : D == 4 ? 0x141 : 0x140;
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), ctrl, 0xF, 0xF, true));
+}
+// Maximum over a row of 16 lanes, all of which must be active.
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, row_other<1>(v));
+  v = fmaxf(v, row_other<2>(v));
+  v = fmaxf(v, row_other<4>(v));
+  return fmaxf(v, row_other<8>(v));
+}
+
 // Wave-wide butterfly reductions (wave64).
 __device__ __forceinline__ float wave_max_xor(float v, int width) {
   for (int o = 1; o < width; o <<= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
@@ -130,7 +145,7 @@ __device__ __forceinline__ uint2 quant_tile_1x128(const float* v, float* scale) 
   float amax = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-  amax = wave_max_xor(amax, 16);
+  amax = row_max(amax);
   const float s = amax > 0.0f ? amax / 448.0f : 1.0f;
   *scale = s;
   if (recip_ok(s)) {

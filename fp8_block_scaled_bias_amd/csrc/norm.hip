@@ -73,9 +73,12 @@ __device__ __forceinline__ void load_f32x8(const float* p, float* f) {
 }
 
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-  return v;
+  v += row_other<1>(v);
+  v += row_other<2>(v);
+  v += row_other<4>(v);
+  v += row_other<8>(v);
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
 }
 
 // Sums over the workgroup of N values a thread, for every thread.  `s` is used
@@ -281,24 +284,24 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBwdArgs a) {
   }
 }
 
-// out[h] = sum over the parts, in order: 16 groups of threads take every 16th
+// out[h] = sum over the parts, in order: RG groups of threads take every RG-th
 // part of 64 columns, their sums meet in LDS.  (P = 0: zero.)
-constexpr int RD = 256;
+constexpr int RG = 64, RD = 16 * RG;
 __global__ __launch_bounds__(RD) void add_parts_kernel(const float* part, int P, int64_t H, float* out) {
-  __shared__ float4 s[16][16];
+  __shared__ float4 s[RG][16];
   const int g = threadIdx.x >> 4, l = threadIdx.x & 15;
   const int64_t col = (int64_t)blockIdx.x * 64 + 4 * l;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (col < H)
 #pragma unroll 8
-    for (int p = g; p < P; p += 16) {
+    for (int p = g; p < P; p += RG) {
       const float4 w = *reinterpret_cast<const float4*>(part + (int64_t)p * H + col);
       v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
     }
   s[g][l] = v;
   __syncthreads();
   if (g || col >= H) return;
-  for (int i = 1; i < 16; ++i) {
+  for (int i = 1; i < RG; ++i) {
     const float4 w = s[i][l];
     v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
   }
@@ -339,38 +342,44 @@ __device__ __forceinline__ uint4 stream16(const uint16_t* p) {
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// Rows and weights of a token (uniform): slot k is the shared row's.
+// (read only here, and the same for every lane: through the scalar cache)
+template <class V>
+__device__ __forceinline__ V scalar(const V* p, int64_t i) {
+  return ((const __attribute__((address_space(4))) V*)p)[i];
+}
+// Rows and weights of a token (uniform): its experts' in the slots below k, the
+// shared row's in the last.  An entry of the permutation outside [0, T k) is
+// kept as it is: it reads the last routed row, and its gradient is not written.
 struct Token {
-  const uint16_t* row[KR];
+  uint32_t row[KR];
   float w[KR];
-  int n;
 };
+__device__ __forceinline__ bool has(const CombineArgs& a, int j) { return j < KR - 1 ? j < a.k : a.S != nullptr; }
 __device__ __forceinline__ Token token_of(const CombineArgs& a, int64_t t) {
   Token o;
-  const uint32_t last = (uint32_t)(a.T * a.k - 1);
+  // (slots past k repeat the last one: all loads at once, none behind a branch)
 #pragma unroll
-  for (int j = 0; j < KR; ++j) {
-    o.row[j] = nullptr;
-    o.w[j] = 0.0f;
-    if (j < a.k) {
-      o.row[j] = a.D + (int64_t)min((uint32_t)a.inv_perm[t * a.k + j], last) * a.H;
-      o.w[j] = a.topk_w[t * a.k + j];
-    } else if (j == a.k && a.S) {
-      o.row[j] = a.S + t * a.H;
-      o.w[j] = a.shared_w ? a.shared_w[t] : 1.0f;
-    }
+  for (int j = 0; j < KR - 1; ++j) {
+    o.row[j] = (uint32_t)scalar(a.inv_perm, t * a.k + min(j, a.k - 1));
+    o.w[j] = scalar(a.topk_w, t * a.k + min(j, a.k - 1));
   }
-  o.n = a.k + (a.S ? 1 : 0);
+  o.row[KR - 1] = (uint32_t)t;
+  const float w = scalar(a.shared_w ? a.shared_w + t : a.topk_w, 0);
+  o.w[KR - 1] = a.shared_w ? w : 1.0f;
   return o;
+}
+__device__ __forceinline__ const uint16_t* row_of(const CombineArgs& a, const Token& tk, int j) {
+  if (j == KR - 1) return a.S + (int64_t)tk.row[j] * a.H;
+  return a.D + (int64_t)min(tk.row[j], (uint32_t)(a.T * a.k - 1)) * a.H;
 }
 
 // z: the rows' sum in slot order
-__device__ __forceinline__ void gather8(const Token& tk, const uint4* rows, float* z) {
+__device__ __forceinline__ void gather8(const CombineArgs& a, const Token& tk, const uint4* rows, float* z) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) z[i] = 0.0f;
 #pragma unroll
   for (int j = 0; j < KR; ++j)
-    if (j < tk.n) {
+    if (has(a, j)) {
       float d[8];
       unpack8(rows[j], d);
 #pragma unroll
@@ -394,9 +403,9 @@ __global__ __launch_bounds__(1024) void combine_norm_kernel(CombineArgs a) {
       uint4 rows[KR];
 #pragma unroll
       for (int j = 0; j < KR; ++j)
-        if (j < tk.n) rows[j] = stream16(tk.row[j] + col);
+        if (has(a, j)) rows[j] = stream16(row_of(a, tk, j) + col);
       res[c] = load8<TYPE>(a.residual, t * H + col);
-      gather8(tk, rows, z[c]);
+      gather8(a, tk, rows, z[c]);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) z[c][i] = 0.0f;
@@ -427,110 +436,144 @@ __global__ __launch_bounds__(1024) void combine_norm_kernel(CombineArgs a) {
   }
 }
 
-template <int NC, int TYPE>
+// A token's rows are held in registers between the sums and the gradients
+// (HOLD); as soon as a row's gradient is formed, the next token's row is loaded
+// in its place.  Without HOLD (H > 8192) they are read twice.  One barrier a
+// token: the dots' parts are added up behind the next one.
+template <int NC, int TYPE, bool HOLD>
 __global__ __launch_bounds__(1024) void combine_norm_backward_kernel(CombineArgs a) {
   __shared__ Sums<2> s_sum;
   __shared__ float s_dot[2][MAXW][KR];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, waves = blockDim.x >> 6;
   const int64_t H = a.H, TK = a.T * a.k;
-  float w[NC][8], dw[NC][8];
+  float dw[NC][8];
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    const int64_t col = ((int64_t)c * blockDim.x + tid) * 8;
+  for (int c = 0; c < NC; ++c)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[c][i] = 0.0f, w[c][i] = 1.0f;
-    if (a.weight && col < H) load_f32x8(a.weight + col, w[c]);
-  }
+    for (int i = 0; i < 8; ++i) dw[c][i] = 0.0f;
+  const uint32_t H32 = (uint32_t)H;
+  auto col_of = [&](int c) -> uint32_t { return ((uint32_t)c * blockDim.x + (uint32_t)tid) * 8; };
+  auto at_row = [&](const void* p, int64_t t) -> const void* {  // (uniform)
+    return static_cast<const uint8_t*>(p) + t * H * (TYPE == MOE_TYPE_F32 ? 4 : 2);
+  };
+  uint4 rows[KR];
+  Raw<TYPE> dy;
+  auto load = [&](const Token& tk, int64_t t, uint32_t col) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < KR; ++j)
+      if (has(a, j)) rows[j] = stream16(row_of(a, tk, j) + col);
+    dy = load8<TYPE>(at_row(a.dy, t), col);
+  };
+  // (through an empty asm, so that the rows stay packed and are not kept as the
+  // 72 values that the passes before unpacked)
+  auto keep_packed = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < KR; ++j)
+      if (has(a, j)) asm volatile("" : "+v"(rows[j].x), "+v"(rows[j].y), "+v"(rows[j].z), "+v"(rows[j].w));
+  };
+  auto weights = [&](uint32_t col, float* w) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+    if (a.weight) load_f32x8(a.weight + col, w);
+  };
+  // d_topk_w and d_shared_w of a token whose waves' dots lie in `slot`
+  auto dots = [&](int64_t t, int slot) __attribute__((always_inline)) {
+    if (tid < a.k || (tid == KR - 1 && a.d_shared_w)) {
+      float v = 0.0f;
+      for (int i = 0; i < waves; ++i) v += s_dot[slot][i][tid];
+      if (tid < a.k) a.d_topk_w[t * a.k + tid] = v;
+      else a.d_shared_w[t] = v;
+    }
+  };
+  const int64_t stride = gridDim.x;
   int slot = 0;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, slot ^= 1) {
-    const Token tk = token_of(a, t);
-    uint4 rows[NC][KR];
-    Raw<TYPE> dy[NC];
-    float z[NC][8], g[NC][8];
+  Token next = token_of(a, blockIdx.x);
+  if (HOLD && col_of(0) < H32) load(next, blockIdx.x, col_of(0));
+  for (int64_t t = blockIdx.x; t < a.T; t += stride, slot ^= 1) {
+    const Token tk = next;
+    const bool more = t + stride < a.T;
+    if (more) next = token_of(a, t + stride);
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int64_t col = ((int64_t)c * blockDim.x + tid) * 8;
-      if (col >= H) continue;
-#pragma unroll
-      for (int j = 0; j < KR; ++j)
-        if (j < tk.n) rows[c][j] = stream16(tk.row[j] + col);
-      dy[c] = load8<TYPE>(a.dy, t * H + col);
-    }
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int64_t col = ((int64_t)c * blockDim.x + tid) * 8;
-      if (col >= H) continue;
-      gather8(tk, rows[c], z[c]);
-      values8<TYPE>(dy[c], g[c]);
+      uint32_t col = col_of(c);
+      asm volatile("" : "+v"(col));  // (so that no address is kept over the loop)
+      if (col >= H32) continue;
+      if (!HOLD) load(tk, t, col);
+      float z[8], g[8], w[8];
+      gather8(a, tk, rows, z);
+      values8<TYPE>(dy, g);
+      weights(col, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        g[c][i] *= a.scale;
-        sum[0] = fmaf(z[c][i], z[c][i], sum[0]);
-        sum[1] = fmaf(g[c][i] * w[c][i], z[c][i], sum[1]);
+        sum[0] = fmaf(z[i], z[i], sum[0]);
+        sum[1] = fmaf(a.scale * g[i] * w[i], z[i], sum[1]);
       }
     }
-    float r = 1.0f, mean = 0.0f;
-    if (a.norm) {
-      block_sums<2>(sum, s_sum, slot, waves);
-      r = rstd_of(sum[0], H, a.eps);
-      mean = r * sum[1] / (float)H;  // of the normed row and its gradient
-    }
+    if (HOLD) keep_packed();
+    block_sums<2>(sum, s_sum, slot, waves);
+    if (t > blockIdx.x) dots(t - stride, slot ^ 1);
+    const float r = a.norm ? rstd_of(sum[0], H, a.eps) : 1.0f;
+    const float mean = a.norm ? r * sum[1] / (float)H : 0.0f;  // of the normed row and its gradient
     float dot[KR];
 #pragma unroll
     for (int j = 0; j < KR; ++j) dot[j] = 0.0f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int64_t col = ((int64_t)c * blockDim.x + tid) * 8;
-      if (col >= H) continue;
+      uint32_t col = col_of(c);
+      asm volatile("" : "+v"(col));  // (so that no address is kept over the loop)
+      if (col >= H32) continue;
+      if (!HOLD) load(tk, t, col);
       float dz[8];
+      {
+        float z[8], g[8], w[8];
+        gather8(a, tk, rows, z);
+        values8<TYPE>(dy, g);
+        weights(col, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float hat = z[c][i] * r;
-        dw[c][i] = fmaf(g[c][i], hat, dw[c][i]);
-        dz[i] = r * fmaf(-mean, hat, g[c][i] * w[c][i]);
+        for (int i = 0; i < 8; ++i) {
+          const float hat = z[i] * r;
+          g[i] *= a.scale;
+          dw[c][i] = fmaf(g[i], hat, dw[c][i]);
+          dz[i] = r * fmaf(-mean, hat, g[i] * w[i]);
+        }
       }
+      if (HOLD && more) dy = load8<TYPE>(at_row(a.dy, t + stride), col);
+      keep_packed();
 #pragma unroll
       for (int j = 0; j < KR; ++j)
-        if (j < tk.n) {
+        if (has(a, j)) {
           float d[8], o[8];
-          unpack8(rows[c][j], d);
+          unpack8(rows[j], d);
+          if (HOLD && more) rows[j] = stream16(row_of(a, next, j) + col);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             dot[j] = fmaf(dz[i], d[i], dot[j]);
             o[i] = tk.w[j] * dz[i];
           }
-          // (a row outside the permutation's range is not written)
-          const int64_t to = j < a.k ? (int64_t)(uint32_t)a.inv_perm[t * a.k + j] : TK + t;
-          if (j < a.k && to >= TK) continue;
-          *reinterpret_cast<uint4*>(a.dD + to * H + col) = pack8(o);
+          if (j < KR - 1 && tk.row[j] >= TK) continue;
+          const int64_t to = (j < KR - 1 ? (int64_t)tk.row[j] : TK + t) * H;
+          *reinterpret_cast<uint4*>(a.dD + to + col) = pack8(o);
           if (a.codes) {
             float s;
-            *reinterpret_cast<uint2*>(a.codes + to * H + col) = quant_tile_1x128(o, &s);
-            if ((tid & 15) == 0) a.scales[(to * H + col) >> 7] = s;
+            *reinterpret_cast<uint2*>(a.codes + to + col) = quant_tile_1x128(o, &s);
+            if ((tid & 15) == 0) a.scales[(to >> 7) + (col >> 7)] = s;
           }
         }
     }
 #pragma unroll
-    for (int j = 0; j < KR; ++j)
-      if (j < tk.n) {
-        dot[j] = wave_sum(dot[j]);
-        if (lane == 0) s_dot[slot][wv][j] = dot[j];
-      }
-    __syncthreads();
-    if (tid < tk.n) {
-      float v = 0.0f;
-      for (int i = 0; i < waves; ++i) v += s_dot[slot][i][tid];
-      if (tid < a.k) a.d_topk_w[t * a.k + tid] = v;
-      else if (a.d_shared_w) a.d_shared_w[t] = v;
-    }
+    for (int j = 0; j < KR; ++j) dot[j] = wave_sum(dot[j]);
+    if (lane == 0)
+#pragma unroll
+      for (int j = 0; j < KR; ++j) s_dot[slot][wv][j] = dot[j];
   }
+  __syncthreads();
+  dots(blockIdx.x + (a.T - 1 - blockIdx.x) / stride * stride, slot ^ 1);
   if (!a.part) return;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int64_t col = ((int64_t)c * blockDim.x + tid) * 8;
-    if (col >= H) continue;
-    float* p = a.part + (int64_t)blockIdx.x * H + col;
+    if (col_of(c) >= H32) continue;
+    float* p = a.part + (int64_t)blockIdx.x * H + col_of(c);
     *reinterpret_cast<float4*>(p) = make_float4(dw[c][0], dw[c][1], dw[c][2], dw[c][3]);
     *reinterpret_cast<float4*>(p + 4) = make_float4(dw[c][4], dw[c][5], dw[c][6], dw[c][7]);
   }
@@ -538,8 +581,12 @@ __global__ __launch_bounds__(1024) void combine_norm_backward_kernel(CombineArgs
 
 constexpr int64_t kMaxH = 16384;
 inline unsigned threads_of(int64_t H, int nc) { return (unsigned)(ceil_div(ceil_div(H, 8 * nc), 64) * 64); }
-// workgroups of a backward pass: at most two a CU
-inline int64_t parts_of(int64_t T) { return std::min<int64_t>(T, 2 * gemm::num_cus()); }
+// Workgroups of a backward pass, each with its part of d_weight: two a CU of 256
+// where a row takes 16 waves, more of shorter rows.
+inline int64_t parts_of(int64_t T, int64_t H) {
+  const int64_t waves = ceil_div(ceil_div(H, 8 * (H <= 8192 ? 1 : 2)), 64);
+  return std::min<int64_t>(T, 512 * std::max<int64_t>(1, std::min<int64_t>(4, 16 / waves)));
+}
 
 bool aligned(const void* p, int n) { return ((uintptr_t)p & (uintptr_t)(n - 1)) == 0; }
 
@@ -602,7 +649,7 @@ extern "C" int moe_norm(const void* x, int32_t x_type, const void* add_bf16, con
 }
 
 extern "C" size_t moe_norm_backward_workspace_bytes(int64_t T, int64_t H) {
-  return T > 0 && H > 0 ? (size_t)(std::min<int64_t>(T, MOE_NORM_MAX_PARTS) * H) * sizeof(float) : 0;
+  return T > 0 && H > 0 ? (size_t)(parts_of(T, H) * H) * sizeof(float) : 0;
 }
 
 extern "C" int moe_norm_backward(const void* dn_bf16, const void* x, int32_t x_type, const float* weight,
@@ -622,7 +669,7 @@ extern "C" int moe_norm_backward(const void* dn_bf16, const void* x, int32_t x_t
                   aligned(d_res, 16) && aligned(dx, 16) && aligned(workspace, 16),
               "moe_norm_backward: tensors and workspace must be 16-byte, rstd 4-byte aligned");
   MOE_INVALID(dx != dn_bf16 && dx != x, "moe_norm_backward: dx must not alias dn or x");
-  const int64_t P = std::min<int64_t>(parts_of(T), MOE_NORM_MAX_PARTS);
+  const int64_t P = parts_of(T, H);
   MOE_REQUIRE(!d_weight || (workspace && workspace_bytes >= moe_norm_backward_workspace_bytes(T, H)),
               MOE_ERR_WORKSPACE, "moe_norm_backward: workspace of %zu bytes, %zu needed", workspace_bytes,
               moe_norm_backward_workspace_bytes(T, H));
@@ -715,7 +762,7 @@ extern "C" int moe_combine_norm_backward(const void* dy, int32_t x_type, const i
                   aligned(d_expert_out_e4m3, 8) && aligned(d_expert_out_scale, 4),
               "%s: tensors and workspace must be 16-byte, codes 8-byte, the rest 4-byte aligned", who);
   MOE_INVALID(d_expert_out_bf16 != expert_out_bf16 && d_expert_out_bf16 != dy, "%s: dD must not alias D or dy", who);
-  const int64_t P = std::min<int64_t>(parts_of(T), MOE_NORM_MAX_PARTS);
+  const int64_t P = parts_of(T, H);
   MOE_REQUIRE(!d_weight || (workspace && workspace_bytes >= moe_norm_backward_workspace_bytes(T, H)),
               MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", who, workspace_bytes,
               moe_norm_backward_workspace_bytes(T, H));
@@ -731,11 +778,11 @@ extern "C" int moe_combine_norm_backward(const void* dy, int32_t x_type, const i
   a.part = d_weight ? static_cast<float*>(workspace) : nullptr;
   const dim3 grid((unsigned)P);
   if (x_type == MOE_TYPE_F32) {
-    if (H <= 8192) combine_norm_backward_kernel<1, MOE_TYPE_F32><<<grid, dim3(threads_of(H, 1)), 0, st>>>(a);
-    else combine_norm_backward_kernel<2, MOE_TYPE_F32><<<grid, dim3(threads_of(H, 2)), 0, st>>>(a);
+    if (H <= 8192) combine_norm_backward_kernel<1, MOE_TYPE_F32, true><<<grid, dim3(threads_of(H, 1)), 0, st>>>(a);
+    else combine_norm_backward_kernel<2, MOE_TYPE_F32, false><<<grid, dim3(threads_of(H, 2)), 0, st>>>(a);
   } else {
-    if (H <= 8192) combine_norm_backward_kernel<1, MOE_TYPE_BF16><<<grid, dim3(threads_of(H, 1)), 0, st>>>(a);
-    else combine_norm_backward_kernel<2, MOE_TYPE_BF16><<<grid, dim3(threads_of(H, 2)), 0, st>>>(a);
+    if (H <= 8192) combine_norm_backward_kernel<1, MOE_TYPE_BF16, true><<<grid, dim3(threads_of(H, 1)), 0, st>>>(a);
+    else combine_norm_backward_kernel<2, MOE_TYPE_BF16, false><<<grid, dim3(threads_of(H, 2)), 0, st>>>(a);
   }
   if (d_weight) add_parts(a.part, P, H, d_weight, st);
   return check_launch(who);

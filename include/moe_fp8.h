@@ -65,9 +65,6 @@ extern "C" {
 #define MOE_QUANT_E4M3       1   /* 1x128 tiles, as fp8_quant_1x128 */
 #define MOE_QUANT_INT8       2   /* one scale a row, as int8_quant_rows */
 
-/* Most parts that a backward norm keeps of d_weight (workspace rows). */
-#define MOE_NORM_MAX_PARTS   512
-
 /* Message of the last failed call on this thread ("" if none). */
 const char* moe_last_error(void);
 

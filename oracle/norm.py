@@ -4,7 +4,7 @@ after the other."""
 import numpy as np
 
 U = 2.0 ** -24
-ADDS = 64
+ADDS = 96
 
 
 def _mean(v, e):

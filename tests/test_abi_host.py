@@ -402,7 +402,8 @@ def test_norm_validation():
     assert nb(dn=odd) == L.MOE_ERR_INVALID and "aligned" in L.last_error()
     assert nb(dx=P[0]) == L.MOE_ERR_INVALID and nb(dx=P[1]) == L.MOE_ERR_INVALID and "alias" in L.last_error()
     need = rc("moe_norm_backward_workspace_bytes", 4, 128)
-    assert need == 4 * 128 * 4 and rc("moe_norm_backward_workspace_bytes", 1 << 20, 128) == 512 * 128 * 4
+    assert need == 4 * 128 * 4 and rc("moe_norm_backward_workspace_bytes", 1 << 20, 128) == 2048 * 128 * 4
+    assert rc("moe_norm_backward_workspace_bytes", 1 << 20, 7168) == 512 * 7168 * 4
     assert rc("moe_combine_norm_backward_workspace_bytes", 4, 128) == need
     assert nb(dw=P[4], ws=P[5], b=need - 1) == L.MOE_ERR_WORKSPACE and str(need) in L.last_error()
     assert nb(dw=P[4]) == L.MOE_ERR_WORKSPACE
