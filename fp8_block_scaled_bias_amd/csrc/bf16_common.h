@@ -41,7 +41,10 @@ __device__ __forceinline__ v16f mfma(const v4i& x, const v4i& y, const v16f& c) 
 // The gate's activation, g times the logistic function of z: z = g (SiLU), or
 // twice the argument of the tanh form of GELU, 2 sqrt(2/pi) (g + 0.044715 g^3).
 // There g is held to +-16, past which the logistic function is 0 or 1 in
-// fp32, so that the slope stays finite for every finite g.
+// fp32, so that the slope stays finite for every finite g.  The exponential and
+// the reciprocal are the hardware's (an ulp each: what the rounding of z itself
+// does to the exponential is more): their exact forms made the epilogue of a 256
+// x 256 tile of gate and up 128 x 30 instructions long instead of 128 x 8.
 constexpr float kGeluR = 1.5957691216057308f, kGeluC = 0.044715f;
 __device__ __forceinline__ float logistic(float g, int act, float* dz) {
   float z = g;
@@ -51,7 +54,7 @@ __device__ __forceinline__ float logistic(float g, int act, float* dz) {
     z = kGeluR * c * fmaf(kGeluC, c2, 1.0f);
     *dz = kGeluR * fmaf(3.0f * kGeluC, c2, 1.0f);
   }
-  return 1.0f / (1.0f + expf(-z));
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
 }
 __device__ __forceinline__ float glu(float g, float u, int act) {
   float dz;

@@ -27,6 +27,7 @@
 // their slots hold is not used: such rows and columns are not stored, such
 // contraction values are cleared in the registers of both operands.
 #include "bf16_common.h"
+#include "bf16_wide_waits.h"
 
 namespace moe {
 namespace bf16 {
@@ -41,7 +42,7 @@ constexpr int WT = 256;
 constexpr int REG = 128 * 128;      // a region: 16 KB
 constexpr int STAGE = 4 * REG;      // A0, A1, B0, B1
 constexpr int STRIP = 8;            // row tiles of a strip
-constexpr int OFF_OUT = 2 * STAGE;  // per wave 32 x 32 results
+constexpr int OFF_OUT = 2 * STAGE;  // per wave 32 rows x 128 B
 constexpr int OFF_PREF = OFF_OUT + 4 * 4096;
 constexpr int OFF_OFFS = OFF_PREF + 4112;
 constexpr int OFF_IDX = OFF_OFFS + 4112;  // int [4][256]
@@ -120,7 +121,7 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
   const int xcd = blockIdx.x & 7, jw = blockIdx.x >> 3, nper = gridDim.x >> 3;
   int64_t tlo, thi;
   if (PT) {
-    constexpr int OVER = 4;  // a tile's stores, in K blocks
+    constexpr int OVER = 8;  // a tile's stores, in K blocks (15 us, 1.8 us a block)
     const int64_t per = mtiles * ntiles, cost = s_pref[G] + (int64_t)OVER * G;
     auto cut = [&](int x) -> int64_t {  // first tile of XCD x
       const int64_t c = cost * x;       // in eighths
@@ -142,37 +143,56 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
   }
   const int64_t L0 = tlo + jw;
   if (L0 >= thi) return;
-  const int my_n = (int)((thi - L0 + nper - 1) / nper);
+  const int my_n = __builtin_amdgcn_readfirstlane((int)((thi - L0 + nper - 1) / nper));
 
-  // tile of ordinal o (past the last: the last); gh: group of the tile before
-  auto tile_at = [&](int& gh, int o) {
-    const int64_t L = L0 + (int64_t)min(o, my_n - 1) * nper;
-    Tile t;
-    uint32_t cnt, rem;
-    if (PT) {
-      const int64_t per = mtiles * ntiles;
-      gh = t.g = __builtin_amdgcn_readfirstlane((int)(L / per));
-      cnt = (uint32_t)mtiles;
-      rem = (uint32_t)(L - t.g * per);
-    } else {
-      int g = gh;
-      while (g + 1 < G && (int64_t)s_pref[g + 1] * ntiles <= L) ++g;
-      gh = t.g = __builtin_amdgcn_readfirstlane(g);
-      cnt = (uint32_t)(s_pref[t.g + 1] - s_pref[t.g]);
-      rem = (uint32_t)(L - (int64_t)s_pref[t.g] * ntiles);
+  // A place in the workgroup's tiles, every nper-th of the XCD's: the group and
+  // the tile's number in it (past the last: the last).  The number of tiles is
+  // far below 2^32, their results being in memory.
+  struct Place {
+    int left, g;
+    uint32_t rem;
+  };
+  const uint32_t per = (uint32_t)(mtiles * ntiles);  // kWgrad: tiles of every group
+  auto tiles_of = [&](int g) -> uint32_t {
+    return PT ? per : (uint32_t)__builtin_amdgcn_readfirstlane(s_pref[g + 1] - s_pref[g]) * (uint32_t)ntiles;
+  };
+  auto settle = [&](Place& c) {
+    uint32_t n = tiles_of(c.g);
+    while (c.rem >= n) {
+      c.rem -= n;
+      n = tiles_of(++c.g);
     }
-    const uint32_t strip = rem / (STRIP * (uint32_t)ntiles), r2 = rem - strip * (STRIP * (uint32_t)ntiles);
+  };
+  auto advance = [&](Place& c) {
+    if (--c.left <= 0) return;
+    c.rem += (uint32_t)nper;
+    settle(c);
+  };
+  auto tile_at = [&](const Place& c) {
+    Tile t;
+    t.g = c.g;
+    const int g0 = __builtin_amdgcn_readfirstlane(s_offs[t.g]), g1 = __builtin_amdgcn_readfirstlane(s_offs[t.g + 1]);
+    const uint32_t cnt = PT ? (uint32_t)mtiles : (uint32_t)(g1 - g0 + 255) >> 8;
+    const uint32_t strip = c.rem / (STRIP * (uint32_t)ntiles), r2 = c.rem - strip * (STRIP * (uint32_t)ntiles);
     const uint32_t w = min((uint32_t)STRIP, cnt - strip * STRIP), nt = r2 / w;
     const int mt = (int)(strip * STRIP + r2 - nt * w);
     t.n0 = __builtin_amdgcn_readfirstlane((int)(nt * TN));
-    const int g0 = s_offs[t.g], g1 = s_offs[t.g + 1];
     t.m0 = __builtin_amdgcn_readfirstlane((PT ? 0 : g0) + mt * 256);
-    t.rows = __builtin_amdgcn_readfirstlane(min(256, (PT ? (int)a.N : g1) - t.m0));
-    t.k0 = __builtin_amdgcn_readfirstlane(g0);
-    t.kc = __builtin_amdgcn_readfirstlane(PT ? g1 - g0 : (int)(QT ? a.N : a.K));
+    t.rows = min(256, (PT ? (int)a.N : g1) - t.m0);
+    t.k0 = g0;
+    t.kc = PT ? g1 - g0 : (int)(QT ? a.N : a.K);
     t.nkb = max(2, (t.kc + 63) >> 6);
     return t;
   };
+  Place first{my_n, 0, 0};
+  if (PT) {
+    first.g = (int)uniform(L0 / per);
+    first.rem = (uint32_t)(L0 - (int64_t)first.g * per);
+  } else {
+    int64_t rem = L0;
+    while (rem >= (int64_t)tiles_of(first.g)) rem -= tiles_of(first.g++);
+    first.rem = (uint32_t)rem;
+  }
   // valid columns of a tile's half h
   auto cols_of = [&](const Tile& t, int h) -> int {
     return (int)min<int64_t>(128, max<int64_t>(0, GLU ? NC - t.n0 : NC - t.n0 - 128 * h));
@@ -202,9 +222,10 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
   }
   const uint32_t a_last = (uint32_t)(a.A_rows - 1);
 
-  // the copies' place: K block ck of the tile of ordinal co
-  int co = 0, ck = 0, cg = 0;
-  Tile ct;
+  // the copies' place: K block ck of tile ct, the co-th; the tile after it
+  int co = 0, ck = 0;
+  Place cp = first;
+  Tile ct, cn = tile_at(cp);
   v4i rp[PT ? 2 : 1], rq[2];
   int* const s_idx = reinterpret_cast<int*>(smem + OFF_IDX);
   // kGlu, kPlain: the row indices of a tile into slot o % 4.  kWgrad: those of
@@ -218,17 +239,23 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
   };
   // kWgrad's index copies run two blocks ahead of the copies that use them: 32
   // copies are issued between, more than a phase's wait leaves on their way
-  int xo = 0, xk = 0, xg = 0, xb = 0, cb = 0;
-  Tile xt;
+  int xk = 0, xb = 0, cb = 0;
+  Place xp = first;
+  int x_k0 = 0, x_kc = 0;  // the group's rows
+  auto index_group = [&]() {
+    x_k0 = __builtin_amdgcn_readfirstlane(s_offs[xp.g]);
+    x_kc = __builtin_amdgcn_readfirstlane(s_offs[xp.g + 1]) - x_k0;
+  };
   auto index_block = [&]() {
-    const int64_t r0 = (int64_t)xt.k0 + 64 * xk;
-    const int left = min(64, xt.kc - 64 * xk);
+    const int64_t r0 = (int64_t)x_k0 + 64 * xk;
+    const int left = min(64, x_kc - 64 * xk);
     copy4(rsrc(a.index + (left > 0 ? r0 : 0), (uint32_t)max(left, 1) * 4), (uint32_t)lane * 4,
           (uint32_t)__builtin_amdgcn_readfirstlane((int)(lds0 + OFF_IDX + wv * 1024 + (xb & 3) * 256)));
     ++xb;
-    if (++xk == xt.nkb) {
+    if (++xk == max(2, (x_kc + 63) >> 6)) {
       xk = 0;
-      xt = tile_at(xg, ++xo);
+      advance(xp);
+      index_group();
     }
   };
   // resources of the K block to be copied, where they move with it
@@ -266,7 +293,9 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
     }
   };
   auto copy_tile = [&]() {  // sources of tile co
-    ct = tile_at(cg, co);
+    ct = cn;
+    advance(cp);
+    cn = tile_at(cp);
     if (!QT) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -294,8 +323,7 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
         const int row = 128 * (p >> 2) + 32 * wv + 8 * (p & 3) + (ln >> 3);
         vp[p] = row < ct.rows ? index_of(co, row) * ldp + (uint32_t)(((ln & 7) ^ swz(row)) << 4) : kOut;
       }
-      int g2 = cg;
-      index_copy(tile_at(g2, co + 1), co + 1);
+      index_copy(cn, co + 1);
     } else {
       rp[0] = rsrc(a.P + (int64_t)ct.m0 * (ldp / 2), (uint32_t)ct.rows * ldp);
     }
@@ -333,7 +361,8 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
 
   // ---- operand reads: lane (q, l32) has 8 contraction values (16 ks + 8 q ..)
   // of row or column l32 of a 32-wide block.  The wave's two blocks of a
-  // region begin at 32 wm (P), 32 wn (Q) and 64 further.
+  // region begin at 32 wm and 64 further (P), at 64 wn and 32 further (Q: 64
+  // columns, a whole line of bf16, are one wave's).
   uint32_t o[4];
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks)
@@ -343,104 +372,204 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
   auto read_one = [&](auto R_, int n, uint32_t st) __attribute__((always_inline)) {
     constexpr int R = decltype(R_)::value;
     const uint8_t* p = smem + st * STAGE + R * REG;
-    const int w = R >= 2 ? wn : wm;
+    const int w = R >= 2 ? 2 * wn + (n & 1) : wm + 2 * (n & 1);  // the 32-wide block
     if (R >= 2 ? QT : PT)
-      fr[R][n & 1][n >> 1] = tr_read(p, otr, w + 2 * (n & 1), n >> 1);
+      fr[R][n & 1][n >> 1] = tr_read(p, otr, w, n >> 1);
     else
-      fr[R][n & 1][n >> 1] = *reinterpret_cast<const v4i*>(p + w * 32 * 128 + o[n >> 1] + (n & 1) * 64 * 128);
+      fr[R][n & 1][n >> 1] = *reinterpret_cast<const v4i*>(p + w * 32 * 128 + o[n >> 1]);
   };
   auto clear_past = [&](auto R_, int left) __attribute__((always_inline)) {
     constexpr int R = decltype(R_)::value;
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      fr[R][0][ks] = keep_first(fr[R][0][ks], left - 16 * ks - 8 * q);
-      fr[R][1][ks] = keep_first(fr[R][1][ks], left - 16 * ks - 8 * q);
-    }
+    for (int ks = 0; ks < 4; ++ks)
+      if (!PT || left < 16 * ks + 16) {
+        fr[R][0][ks] = keep_first(fr[R][0][ks], left - 16 * ks - 8 * q);
+        fr[R][1][ks] = keep_first(fr[R][1][ks], left - 16 * ks - 8 * q);
+      }
   };
 
   v16f acc[2][2][2][2];  // [A half][B half][A block][B block]
 
-  // ---- epilogue.  Lane (q, l32) holds row l32 of a block and its columns 8 e
-  // + 4 q .. +3; through the wave's own 4 KB of LDS (16-byte chunk c of a
-  // row in slot c ^ row % 8) a lane gets 8 columns of rows lane / 4 and + 16.
-  const uint32_t e_wr = OFF_OUT + wv * 4096 + l32 * 128;
-  const uint32_t e_rd = OFF_OUT + wv * 4096 + (lane >> 2) * 128;
-  auto turn = [&](const v16f& c, float (&v)[2][8]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      *reinterpret_cast<float4*>(smem + e_wr + (((2 * e + q) ^ (l32 & 7)) << 4)) =
-          make_float4(c[4 * e], c[4 * e + 1], c[4 * e + 2], c[4 * e + 3]);
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float4 w = *reinterpret_cast<const float4*>(
-            smem + e_rd + r * 2048 + (((2 * (lane & 3) + h) ^ ((lane >> 2) & 7)) << 4));
-        v[r][4 * h] = w.x, v[r][4 * h + 1] = w.y, v[r][4 * h + 2] = w.z, v[r][4 * h + 3] = w.w;
-      }
-  };
+  // ---- epilogue, between MFMAs: A0's results while the last K block works on
+  // A1, A1's while the next tile's first works on A0, a half over 16 slots.
+  // Lane (q, l32) holds row l32 of a 32 x 32 block and its columns 8 e + 4 q ..
+  // +3; a panel of 32 rows by 128 bytes goes through the wave's own 4 KB of LDS
+  // (16-byte chunk c of a row in slot c ^ row % 8) and comes back as 8 whole lines
+  // a store: stores of 32 rows by 32 bytes drain at 34 B/ns a CU instead of 130.
+  // Rows past the tile's end lie outside the store's resource, columns past it
+  // are put outside: every panel issues all its stores.
   typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-  auto pack8 = [](const float* v) {
-    return v4u{f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]), f32x2_to_bf16x2(v[4], v[5]),
-               f32x2_to_bf16x2(v[6], v[7])};
+  const uint32_t ldo = (uint32_t)(MODE == kDgradGlu ? 2 * NC : NC);  // columns of the output's rows
+  // rows r0 .. of a tile in a tensor of `ld` columns a row, from column c0
+  auto rows_at = [&](auto* base, const Tile& t, uint32_t ld, int64_t c0, int r0) __attribute__((always_inline)) {
+    const int64_t row = (MODE == kWgrad ? (int64_t)t.g * a.N : 0) + t.m0 + r0;
+    const int64_t left = max<int64_t>(0, (int64_t)(t.rows - r0) * ld - c0);
+    return __builtin_amdgcn_make_buffer_rsrc((void*)(base + row * ld + c0), 0,
+                                             (int)(uint32_t)(left * (int64_t)sizeof(*base)), 0x00020000);
   };
-  auto unpack8 = [](const v4u& w, float* v) {
+  const uint32_t l7 = l32 & 7;
+  const uint32_t e_wr = OFF_OUT + wv * 4096 + l32 * 128;
+  const uint32_t e_rd = OFF_OUT + wv * 4096 + (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4);
+  v4u lines[4];
+  auto read_lines = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = bf16_to_f32(w[i] & 0xFFFFu), v[2 * i + 1] = bf16_to_f32(w[i] >> 16);
+    for (int r = 0; r < 4; ++r) lines[r] = *reinterpret_cast<const v4u*>(smem + e_rd + r * 1024);
   };
-  auto finish = [&](const Tile& t) __attribute__((always_inline)) {
+  // a panel's lines: rows r0 + 8 r + lane / 8, bytes 16 (lane % 8) of columns cc ..
+  auto store_lines = [&](auto* base, const Tile& t, uint32_t ld, int64_t half, int r0, int cc) __attribute__((always_inline)) {
+    constexpr int SZ = sizeof(*base), per = 16 / SZ;  // columns of a lane
+    const auto out = rows_at(base, t, ld, half + t.n0, r0);
+    const int c = cc + per * (lane & 7);
+    const uint32_t off = t.n0 + c < NC ? ((lane >> 3) * ld + c) * SZ : kOut;
 #pragma unroll
-    for (int H = 0; H < 2; ++H)
+    for (int r = 0; r < 4; ++r)  // (past the rows' end stays past it: kOut + 24 rows is under 2^32)
+      __builtin_amdgcn_raw_buffer_store_b128(lines[r], out, off == kOut ? off : off + 8 * r * ld * SZ, 0, 0);
+  };
+  auto put4 = [&](int chunk, const float* v) __attribute__((always_inline)) {  // 4 bf16 at 8 q of a chunk
+    *reinterpret_cast<uint2*>(smem + e_wr + ((chunk ^ l7) << 4) + 8 * q) = pack4(v);
+  };
+  auto quad = [&](const v16f& c, int e, float (&v)[4]) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+    for (int r = 0; r < 4; ++r) v[r] = c[4 * e + r];
+  };
+  // kDgradGlu: a block's gate and up values as its results are read back, rows
+  // lane / 4 and + 16, columns 8 (lane % 4) ..; loaded a block ahead
+  v4u gate[2][2], up[2][2];
+  auto fetch = [&](auto K_, const Tile& t) __attribute__((always_inline)) {
+    constexpr int K = decltype(K_)::value, H = K >> 3, B = (K >> 2) & 1, i = (K >> 1) & 1, j = K & 1;
+    const int r0 = 128 * H + 64 * i + 32 * wm, c = 128 * B + 64 * wn + 32 * j + 8 * (lane & 3);
+    const auto g = rows_at(a.gu_in, t, ldo, t.n0, r0), u = rows_at(a.gu_in, t, ldo, NC + t.n0, r0);
 #pragma unroll
-        for (int B = 0; B < (GLU ? 1 : 2); ++B)
+    for (int r = 0; r < 2; ++r) {
+      const uint32_t off = t.n0 + c < NC ? ((16 * r + (lane >> 2)) * ldo + c) * 2 : kOut;
+      gate[K & 1][r] = __builtin_amdgcn_raw_buffer_load_b128(g, off, 0, 0);
+      up[K & 1][r] = __builtin_amdgcn_raw_buffer_load_b128(u, off, 0, 0);
+    }
+  };
+  // slot S (0..15) of half H's epilogue
+  auto emit = [&](auto H_, auto S_, const Tile& t) __attribute__((always_inline)) {
+    constexpr int H = decltype(H_)::value, S = decltype(S_)::value;
+    float v[4], w[4];
+    if constexpr (MODE == kWgrad) {
+      // 8 panels, the 32 x 32 blocks; two slots each write half of its quads
+      constexpr int K = S >> 1, B = K >> 2, i = (K >> 1) & 1, j = K & 1;
+      auto store = [&](auto P_) __attribute__((always_inline)) {
+        constexpr int P = decltype(P_)::value;
+        read_lines();
+        store_lines(static_cast<float*>(a.out), t, ldo, 0, 128 * H + 64 * ((P >> 1) & 1) + 32 * wm,
+                    128 * (P >> 2) + 64 * wn + 32 * (P & 1));
+      };
+      if constexpr (S > 0 && S % 2 == 0) store(ic<K - 1>());
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int r0 = 128 * H + 64 * i + 32 * wm + (lane >> 2);
-            const int64_t c = t.n0 + 128 * B + 64 * j + 32 * wn + 8 * (lane & 3);
-            float v[2][8], w[2][8];
-            turn(acc[H][B][i][j], v);
-            if (GLU) turn(acc[H][1][i][j], w);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              if (r0 + 16 * r >= t.rows || c >= NC) continue;
-              const int64_t row = (int64_t)t.m0 + r0 + 16 * r;
-              if (MODE == kWgrad) {
-                float4* out = reinterpret_cast<float4*>(static_cast<float*>(a.out) + ((int64_t)t.g * a.N + row) * NC + c);
-                out[0] = make_float4(v[r][0], v[r][1], v[r][2], v[r][3]);
-                out[1] = make_float4(v[r][4], v[r][5], v[r][6], v[r][7]);
-              } else if (MODE == kGlu) {
-                if (a.keep) {
-                  *reinterpret_cast<v4u*>(a.keep + row * 2 * NC + c) = pack8(v[r]);
-                  *reinterpret_cast<v4u*>(a.keep + row * 2 * NC + NC + c) = pack8(w[r]);
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[r][k] = glu(v[r][k], w[r][k], a.act);
-                *reinterpret_cast<v4u*>(static_cast<uint16_t*>(a.out) + row * NC + c) = pack8(v[r]);
-              } else if (MODE == kDgradGlu) {
-                float g[8], u[8];
-                unpack8(*reinterpret_cast<const v4u*>(a.gu_in + row * 2 * NC + c), g);
-                unpack8(*reinterpret_cast<const v4u*>(a.gu_in + row * 2 * NC + NC + c), u);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) glu_backward(g[k], u[k], v[r][k], a.act, &v[r][k], &w[r][k]);
-                uint16_t* out = static_cast<uint16_t*>(a.out) + row * 2 * NC + c;
-                *reinterpret_cast<v4u*>(out) = pack8(v[r]);
-                *reinterpret_cast<v4u*>(out + NC) = pack8(w[r]);
-              } else {
-                *reinterpret_cast<v4u*>(static_cast<uint16_t*>(a.out) + row * NC + c) = pack8(v[r]);
-              }
-            }
+      for (int e = 2 * (S & 1); e < 2 * (S & 1) + 2; ++e) {
+        quad(acc[H][B][i][j], e, v);
+        *reinterpret_cast<float4*>(smem + e_wr + (((2 * e + q) ^ l7) << 4)) = make_float4(v[0], v[1], v[2], v[3]);
+      }
+      if constexpr (S == 15) store(ic<7>());
+    } else if constexpr (MODE == kGlu) {
+      // 2 row blocks; the kept gate and up panels in the first four slots, h's
+      // quads in the last four
+      constexpr int i = S >> 3, n = S & 7;
+      const int r0 = 128 * H + 64 * i + 32 * wm;
+      uint16_t* const h = static_cast<uint16_t*>(a.out);
+      if constexpr (n == 0 && i == 1) {
+        read_lines();
+        store_lines(h, t, ldo, 0, r0 - 64, 64 * wn);
+      }
+      if constexpr (n < 4) {
+        if (a.keep) {
+          if constexpr (n == 2) {
+            read_lines();
+            store_lines(a.keep, t, 2 * ldo, 0, r0, 64 * wn);
           }
+#pragma unroll
+          for (int k = 4 * (n & 1); k < 4 * (n & 1) + 4; ++k) {
+            quad(acc[H][n >> 1][i][k >> 2], k & 3, v);
+            put4(k, v);
+          }
+        }
+      } else {
+        if constexpr (n == 4)
+          if (a.keep) {
+            read_lines();
+            store_lines(a.keep, t, 2 * ldo, NC, r0, 64 * wn);
+          }
+#pragma unroll
+        for (int k = 2 * (n - 4); k < 2 * (n - 4) + 2; ++k) {
+          quad(acc[H][0][i][k >> 2], k & 3, v);
+          quad(acc[H][1][i][k >> 2], k & 3, w);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] = glu(v[r], w[r], a.act);
+          put4(k, v);
+        }
+        if constexpr (S == 15) {
+          read_lines();
+          store_lines(h, t, ldo, 0, r0, 64 * wn);
+        }
+      }
+    } else if constexpr (MODE == kDgradGlu) {
+      // 8 blocks: dh through LDS as fp32, 8 columns a lane, in the first slot,
+      // gradients in the second
+      constexpr int K = S >> 1, B = K >> 2, i = (K >> 1) & 1, j = K & 1;
+      if constexpr (S % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          quad(acc[H][B][i][j], e, v);
+          *reinterpret_cast<float4*>(smem + e_wr + (((2 * e + q) ^ l7) << 4)) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+        if constexpr (8 * H + K + 1 < 16) fetch(ic<(8 * H + K + 1) & 15>(), t);
+      } else {
+        constexpr int F = K & 1;
+        uint16_t* const out = static_cast<uint16_t*>(a.out);
+        const int r0 = 128 * H + 64 * i + 32 * wm, c = 128 * B + 64 * wn + 32 * j + 8 * (lane & 3);
+        const auto og = rows_at(out, t, ldo, t.n0, r0), ou = rows_at(out, t, ldo, NC + t.n0, r0);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = 16 * r + (lane >> 2);
+          float d[8], dg[8], du[8];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float4 f = *reinterpret_cast<const float4*>(smem + OFF_OUT + wv * 4096 + row * 128 +
+                                                              (((2 * (lane & 3) + x) ^ (row & 7)) << 4));
+            d[4 * x] = f.x, d[4 * x + 1] = f.y, d[4 * x + 2] = f.z, d[4 * x + 3] = f.w;
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t gw = gate[F][r][k >> 1], uw = up[F][r][k >> 1];
+            glu_backward(bf16_to_f32(k & 1 ? gw >> 16 : gw & 0xFFFFu), bf16_to_f32(k & 1 ? uw >> 16 : uw & 0xFFFFu),
+                         d[k], a.act, &dg[k], &du[k]);
+          }
+          const uint2 g0 = pack4(dg), g1 = pack4(dg + 4), u0 = pack4(du), u1 = pack4(du + 4);
+          const uint32_t off = t.n0 + c < NC ? (row * ldo + c) * 2 : kOut;
+          __builtin_amdgcn_raw_buffer_store_b128(v4u{g0.x, g0.y, g1.x, g1.y}, og, off, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(v4u{u0.x, u0.y, u1.x, u1.y}, ou, off, 0, 0);
+        }
+      }
+    } else {
+      // 4 panels of two 32 x 32 blocks; four slots each write a quarter
+      constexpr int K = S >> 2, B = K >> 1, i = K & 1, n = S & 3;
+      auto store = [&](auto P_) __attribute__((always_inline)) {
+        constexpr int P = decltype(P_)::value;
+        read_lines();
+        store_lines(static_cast<uint16_t*>(a.out), t, ldo, 0, 128 * H + 64 * (P & 1) + 32 * wm,
+                    128 * (P >> 1) + 64 * wn);
+      };
+      if constexpr (S > 0 && n == 0) store(ic<K - 1>());
+#pragma unroll
+      for (int k = 2 * n; k < 2 * n + 2; ++k) {
+        quad(acc[H][B][i][k >> 2], k & 3, v);
+        put4(k, v);
+      }
+      if constexpr (S == 15) store(ic<3>());
+    }
   };
 
   // ---- prologue: the first two K blocks, in the order they are read
-  int t_g = 0, to = 0;
-  Tile t = tile_at(t_g, 0);
+  Place p = first;
+  Tile t = cn;
   if (GATHER) {
     if (PT) {
-      xt = t;
-      xg = t_g;
+      index_group();
       index_block();
       index_block();
       index_block();
@@ -472,18 +601,18 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
   barrier();
   copy_next();
   copy_region(ic<0>(), 0);  // A0 of the third
-  wait_copies<20>();
+  // (the first tile's phases wait as every tile's do, for stores of a tile
+  // before it that it does not have: both blocks have landed here)
+  wait_copies<4>();
   barrier();
 
   // A phase: MFMAs of A half H and B half B; reads region R of stage rst for
   // the next one (early, so that the wait at its end finds them done), copies
-  // region CR into stage cst.  FIRST: from zero.  The wait that ends it leaves
-  // the newest 24 on their way, the copies of six phases: what the next phase
-  // reads was copied before them.  Stores and index copies among them make
-  // the wait stricter.
-  auto phase = [&](auto H_, auto B_, auto R_, uint32_t rst, auto CR_, uint32_t cst, auto FIRST_)
-                   __attribute__((always_inline)) {
-    constexpr int H = decltype(H_)::value, B = decltype(B_)::value;
+  // region CR into stage cst.  FIRST: from zero.  PART 0, 1: part of the
+  // epilogue of the other half of d.  W: the wait that ends the phase.
+  auto phase = [&](auto H_, auto B_, auto R_, uint32_t rst, auto CR_, uint32_t cst, auto FIRST_, auto PART_, auto W_,
+                   const Tile& d) __attribute__((always_inline)) {
+    constexpr int H = decltype(H_)::value, B = decltype(B_)::value, PART = decltype(PART_)::value;
     constexpr bool FIRST = decltype(FIRST_)::value;
     auto slot = [&](auto N_) __attribute__((always_inline)) {
       constexpr int n = decltype(N_)::value;
@@ -499,6 +628,7 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
       } else {
         copy_rows(CR_, ic<(n & 3)>(), cst);
       }
+      if constexpr (PART >= 0) emit(ic<1 - H>(), ic<8 * (PART & 1) + n>(), d);
       __builtin_amdgcn_sched_barrier(0);
     };
     slot(ic<0>());
@@ -509,31 +639,55 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
     slot(ic<5>());
     slot(ic<6>());
     slot(ic<7>());
-    wait_copies<24>();
+    wait_copies<decltype(W_)::value>();
     __builtin_amdgcn_sched_barrier(0);
     barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
+  // Ends of phases: the phase's reads are in registers, the copies that the
+  // next phase reads have landed (bf16_wide_waits.h).
   uint32_t st = 0;  // stage of the K block being multiplied
-  auto block = [&](auto FIRST_, int left) __attribute__((always_inline)) {
-    if (left < 64) {
+  Tile done = t;    // the tile before, whose A1 is still to be stored
+  done.rows = 0;
+  auto block = [&](auto FIRST_, auto LAST_, int left) __attribute__((always_inline)) {
+    constexpr bool FIRST = decltype(FIRST_)::value, LAST = decltype(LAST_)::value;
+    const bool cut = (FIRST || LAST) && left < 64;  // (those between are whole)
+    if (cut) {
       clear_past(ic<0>(), left);
       clear_past(ic<2>(), left);
     }
-    phase(ic<0>(), ic<0>(), ic<3>(), st, ic<2>(), st, FIRST_);
-    if (left < 64) clear_past(ic<3>(), left);
-    phase(ic<0>(), ic<1>(), ic<1>(), st, ic<3>(), st, FIRST_);
-    if (left < 64) clear_past(ic<1>(), left);
-    phase(ic<1>(), ic<0>(), ic<0>(), st ^ 1, ic<1>(), st, FIRST_);
+    phase(ic<0>(), ic<0>(), ic<3>(), st, ic<2>(), st, FIRST_, ic<(FIRST ? 0 : -1)>(),
+          ic<waits::phase(MODE, FIRST, LAST, 0)>(), done);
+    if (cut) clear_past(ic<3>(), left);
+    phase(ic<0>(), ic<1>(), ic<1>(), st, ic<3>(), st, FIRST_, ic<(FIRST ? 1 : -1)>(),
+          ic<waits::phase(MODE, FIRST, LAST, 1)>(), done);
+    if (cut) clear_past(ic<1>(), left);
+    if constexpr (LAST) {
+      done = t;
+      if constexpr (MODE == kDgradGlu) {
+        fetch(ic<0>(), done);
+      }
+    }
+    phase(ic<1>(), ic<0>(), ic<0>(), st ^ 1, ic<1>(), st, FIRST_, ic<(LAST ? 0 : -1)>(),
+          ic<waits::phase(MODE, FIRST, LAST, 2)>(), done);
     copy_next();
-    phase(ic<1>(), ic<1>(), ic<2>(), st ^ 1, ic<0>(), st ^ 1, FIRST_);
+    phase(ic<1>(), ic<1>(), ic<2>(), st ^ 1, ic<0>(), st ^ 1, FIRST_, ic<(LAST ? 1 : -1)>(),
+          ic<waits::phase(MODE, FIRST, LAST, 3)>(), done);
     st ^= 1;
   };
-  for (; to < my_n; t = tile_at(t_g, ++to)) {
-    block(ic<1>(), t.kc);
-    for (int k = 1; k < t.nkb; ++k) block(ic<0>(), t.kc - 64 * k);
-    finish(t);
+  for (; p.left > 0; advance(p), t = tile_at(p)) {
+    block(ic<1>(), ic<0>(), t.kc);
+    for (int k = 1; k < t.nkb - 1; ++k) block(ic<0>(), ic<0>(), 64);
+    block(ic<0>(), ic<1>(), t.kc - 64 * (t.nkb - 1));
   }
+  auto flush = [&](auto N_) __attribute__((always_inline)) {
+    emit(ic<1>(), N_, done);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  flush(ic<0>()); flush(ic<1>()); flush(ic<2>()); flush(ic<3>());
+  flush(ic<4>()); flush(ic<5>()); flush(ic<6>()); flush(ic<7>());
+  flush(ic<8>()); flush(ic<9>()); flush(ic<10>()); flush(ic<11>());
+  flush(ic<12>()); flush(ic<13>()); flush(ic<14>()); flush(ic<15>());
   wait_copies<0>();  // what was copied past the last tile lands before the LDS is released
 }
 
