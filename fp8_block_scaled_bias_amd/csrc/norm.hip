@@ -122,11 +122,15 @@ struct NormArgs {
   float* scales;
 };
 
+// (of rows_grid; past the last row there is none)
+__device__ __forceinline__ int64_t row_index() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 template <int NC, int TYPE, int QUANT>
 __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a) {
   __shared__ Sums<1> s_sum, s_max;
   const int tid = threadIdx.x, waves = blockDim.x >> 6;
-  const int64_t t = blockIdx.x, H = a.H, row = t * H;
+  const int64_t t = row_index(), H = a.H, row = t * H;
+  if (t >= a.T) return;
   float v[NC][8];
   float acc[1] = {0.0f};
 #pragma unroll
@@ -391,7 +395,8 @@ template <int NC, int TYPE>
 __global__ __launch_bounds__(1024) void combine_norm_kernel(CombineArgs a) {
   __shared__ Sums<1> s_sum;
   const int tid = threadIdx.x, waves = blockDim.x >> 6;
-  const int64_t t = blockIdx.x, H = a.H;
+  const int64_t t = row_index(), H = a.H;
+  if (t >= a.T) return;
   const Token tk = token_of(a, t);
   float z[NC][8];
   Raw<TYPE> res[NC];
@@ -580,6 +585,12 @@ __global__ __launch_bounds__(1024) void combine_norm_backward_kernel(CombineArgs
 }
 
 constexpr int64_t kMaxH = 16384;
+// A workgroup a row: a dimension of a grid holds less than 2^32 threads, 2^21 rows of
+// up to 1024 are one of 2^31, and further rows go along y.
+inline dim3 rows_grid(int64_t T) {
+  const int64_t x = std::min<int64_t>(T, (int64_t)1 << 21);
+  return dim3((unsigned)x, (unsigned)ceil_div(T, x));
+}
 inline unsigned threads_of(int64_t H, int nc) { return (unsigned)(ceil_div(ceil_div(H, 8 * nc), 64) * 64); }
 // Workgroups of a backward pass, each with its part of d_weight: two a CU of 256
 // where a row takes 16 waves, more of shorter rows.
@@ -606,7 +617,7 @@ void add_parts(const float* part, int64_t P, int64_t H, float* out, hipStream_t 
 
 template <int NC, int TYPE>
 void launch_norm(const NormArgs& a, int quant, hipStream_t st) {
-  const dim3 grid((unsigned)a.T), block(threads_of(a.H, NC));
+  const dim3 grid = rows_grid(a.T), block(threads_of(a.H, NC));
   if (quant == MOE_QUANT_E4M3) norm_kernel<NC, TYPE, MOE_QUANT_E4M3><<<grid, block, 0, st>>>(a);
   else if (quant == MOE_QUANT_INT8) norm_kernel<NC, TYPE, MOE_QUANT_INT8><<<grid, block, 0, st>>>(a);
   else norm_kernel<NC, TYPE, MOE_QUANT_NONE><<<grid, block, 0, st>>>(a);
@@ -718,7 +729,7 @@ extern "C" int moe_combine_norm(const void* expert_out_bf16, const int32_t* inv_
   a.norm = norm, a.weight = weight, a.eps = eps;
   a.T = T, a.H = H, a.k = k, a.y = y, a.rstd = norm ? rstd : nullptr;
   hipStream_t st = as_stream(stream);
-  const dim3 grid((unsigned)T);
+  const dim3 grid = rows_grid(T);
   if (x_type == MOE_TYPE_F32) {
     if (H <= 8192) combine_norm_kernel<1, MOE_TYPE_F32><<<grid, dim3(threads_of(H, 1)), 0, st>>>(a);
     else combine_norm_kernel<2, MOE_TYPE_F32><<<grid, dim3(threads_of(H, 2)), 0, st>>>(a);
