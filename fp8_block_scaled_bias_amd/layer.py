@@ -848,6 +848,8 @@ class MoEBlock:
         this T and type (buffers(T, x.dtype).sum holds v after an add)."""
         layer, s = self.layer, self.layer.shape
         layer._check_gate(seq_len)
+        if keep_gu and isinstance(layer, Int8MoELayer):
+            raise ValueError("keep_gu is for the backward, which an Int8MoELayer does not have")
         T = x.shape[0]
         f, b = self.buffers(T, x.dtype), layer.buffers(T)
         st = stream if stream is not None else torch.cuda.current_stream()
@@ -883,6 +885,8 @@ class MoEBlock:
             raise ValueError(f"dy {tuple(dy.shape)} {dy.dtype} and x {tuple(x.shape)} {x.dtype} differ")
         T = dy.shape[0]
         f, b, bb = self.buffers(T, dy.dtype).gradients(), layer.buffers(T), layer.backward_buffers(T)
+        if T and not f.added and x.data_ptr() == f.y.data_ptr():
+            raise ValueError("x is the block's own y, which the forward has written over: pass a copy of it to both")
         st = stream if stream is not None else torch.cuda.current_stream()
         weighted = self.post_weight is not None
         L.moe_combine_norm_backward(

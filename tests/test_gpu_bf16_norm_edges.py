@@ -5,11 +5,14 @@ import pytest
 import torch
 
 import fp8_block_scaled_bias_amd as M
+import synth
 from bf16_cases import U, check, offsets, up, values
 from bf16_plan import plan
 from gpu_common import bf16_values_host, dev, host, log
 from oracle import bf16 as OB
 from oracle import norm as ON
+from test_gpu_bf16_layer import bf16_layer
+from test_gpu_gate_int8_layers import build
 from test_gpu_norm import EPS
 
 pytestmark = pytest.mark.gpu
@@ -176,3 +179,22 @@ def test_bindings_refuse_wrong_tensors():
         M.moe_norm(x.cpu(), None, None, 4, 64, EPS, None, x)
     with pytest.raises(ValueError):
         M.moe_norm(torch.zeros((64, 4), dtype=torch.bfloat16, device="cuda").t(), None, None, 4, 64, EPS, None, x)
+
+
+def test_block_on_its_own_output():
+    """Forward in place over y; its backward, whose x is gone, is refused."""
+    cfg = synth.CONFIGS["tiny"]
+    block = M.MoEBlock(bf16_layer(cfg)[0])
+    x = up(values(np.random.default_rng(5), (cfg.T, cfg.H)))
+    y1 = block.forward(x).clone()
+    want = block.forward(y1).clone()
+    block.forward(x)
+    y = block.forward(block.buffers(cfg.T, x.dtype).y)
+    assert torch.equal(y, want)
+    with pytest.raises(ValueError, match="written over"):
+        block.backward(x, y)
+    block.forward(y1)
+    block.backward(x, y1)
+    blk = M.MoEBlock(build(M.Int8MoELayer, synth.CONFIGS["mid"], None)[0])
+    with pytest.raises(ValueError, match="keep_gu"):
+        blk.forward(torch.zeros((4, synth.CONFIGS["mid"].H), device="cuda"), keep_gu=True)
