@@ -19,9 +19,9 @@
 //    and is read transposed.
 //  * Copies run on across tiles.  Persistent workgroups; those of an XCD share
 //    a contiguous range of tiles (kWgrad: of equal work, its groups' lengths
-//    differ), numbered in strips of 8 row tiles, column tile by column tile,
-//    so that the 32 tiles at work on an XCD read 8 row and 4 column panels
-//    through its L2.
+//    differ), numbered in strips of 8 row tiles (kWgrad: 3), column tile by
+//    column tile, so that the 32 tiles at work on an XCD read 8 row and 4 column
+//    panels through its L2.
 // Every copy goes through a buffer resource over the rows it may touch; lanes
 // past a tile's or the contraction's end have an offset outside it.  What
 // their slots hold is not used: such rows and columns are not stored, such
@@ -41,7 +41,6 @@ using gemm::swz;
 constexpr int WT = 256;
 constexpr int REG = 128 * 128;      // a region: 16 KB
 constexpr int STAGE = 4 * REG;      // A0, A1, B0, B1
-constexpr int STRIP = 8;            // row tiles of a strip
 constexpr int OFF_OUT = 2 * STAGE;  // per wave 32 rows x 128 B
 constexpr int OFF_PREF = OFF_OUT + 4 * 4096;
 constexpr int OFF_OFFS = OFF_PREF + 4112;
@@ -113,6 +112,12 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
   constexpr int TN = GLU ? 128 : 256;             // output columns of a tile
   const int64_t ntiles = (NC + TN - 1) / TN;
   const int64_t q_rows = GLU ? 2 * a.N : a.N;     // weight rows of a group
+  // Row tiles of a strip.  kWgrad: 32 tiles side by side are 3 x 11, so that what
+  // they store at a time are long pieces of few rows (8192 tokens, 65 groups: 8
+  // 4.02 ms, 4 3.90, 3 3.90, 2 3.94; 64 groups of 896 rows: 3.75, 3.63, 3.50, 3.52);
+  // the other modes read less with squares (gate+up of the same: 8 3.04, 4 3.12, 3
+  // 3.18 ms).
+  constexpr int STRIP = MODE == kWgrad ? 3 : 8;
   const int64_t mtiles = (a.N + 255) / 256;       // kWgrad: row tiles of a group
 
   // kWgrad: s_pref counts the groups' K blocks and a tile's other work in them
@@ -415,6 +420,11 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) lines[r] = *reinterpret_cast<const v4u*>(smem + e_rd + r * 1024);
   };
+  // A weight gradient is more than the caches hold: its stores are marked as not
+  // reused, so that they do not push the operands' panels out of an XCD's 4 MB of
+  // L2 (8192 tokens, 65 groups: 4.35 -> 4.10 ms; no difference for the other
+  // modes, whose results the next call reads).
+  constexpr int CACHE = MODE == kWgrad ? 2 : 0;
   // a panel's lines: rows r0 + 8 r + lane / 8, bytes 16 (lane % 8) of columns cc ..
   auto store_lines = [&](auto* base, const Tile& t, uint32_t ld, int64_t half, int r0, int cc) __attribute__((always_inline)) {
     constexpr int SZ = sizeof(*base), per = 16 / SZ;  // columns of a lane
@@ -423,7 +433,7 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
     const uint32_t off = t.n0 + c < NC ? ((lane >> 3) * ld + c) * SZ : kOut;
 #pragma unroll
     for (int r = 0; r < 4; ++r)  // (past the rows' end stays past it: kOut + 24 rows is under 2^32)
-      __builtin_amdgcn_raw_buffer_store_b128(lines[r], out, off == kOut ? off : off + 8 * r * ld * SZ, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(lines[r], out, off == kOut ? off : off + 8 * r * ld * SZ, 0, CACHE);
   };
   auto put4 = [&](int chunk, const float* v) __attribute__((always_inline)) {  // 4 bf16 at 8 q of a chunk
     *reinterpret_cast<uint2*>(smem + e_wr + ((chunk ^ l7) << 4) + 8 * q) = pack4(v);
