@@ -789,7 +789,7 @@ class BlockBuffers:
         self.n = torch.empty((T, shape.H), dtype=torch.bfloat16, device=dev)
         self.rstd = torch.empty((T,), dtype=f32, device=dev)
         self.y = torch.empty((T, shape.H), dtype=dtype, device=dev)
-        self.added = False
+        self.added = None   # (True or False after a forward)
         self._sum = self.dx = None
 
     @property
@@ -828,6 +828,9 @@ class MoEBlock:
 
     def __init__(self, layer: MoELayer, weight=None, eps: float = 1e-6, post_norm: bool = False,
                  post_weight=None, residual_scale: float = 1.0, scale: float = 1.0):
+        for w in (weight, post_weight):
+            if w is not None and w.shape != (layer.shape.H,):
+                raise ValueError(f"a norm's weight has the shape [H] = [{layer.shape.H}], not {list(w.shape)}")
         self.layer, self.weight, self.eps = layer, weight, eps
         self.post_norm, self.post_weight = post_norm, post_weight
         self.residual_scale, self.scale = residual_scale, scale
@@ -839,6 +842,13 @@ class MoEBlock:
             self._bufs[key] = BlockBuffers(self.layer.shape, T, dtype, self.layer.centroids.device)
         return self._bufs[key]
 
+    def _check_shapes(self, x, add, shared_w):
+        H = self.layer.shape.H
+        if x.dim() != 2 or x.shape[1] != H or (add is not None and add.shape != x.shape):
+            raise ValueError(f"x {list(x.shape)}{'' if add is None else f' and add {list(add.shape)}'}: not [T, {H}]")
+        if shared_w is not None and shared_w.shape != (x.shape[0],):
+            raise ValueError(f"shared_w {list(shared_w.shape)}: not [{x.shape[0]}]")
+
     def forward(self, x, add=None, shared_w=None, stream=None, update_bias: bool = False,
                 gamma: float = 0.001, seq_len: int | None = None, alpha: float = 0.0001,
                 keep_gu: bool = False) -> torch.Tensor:
@@ -848,6 +858,7 @@ class MoEBlock:
         this T and type (buffers(T, x.dtype).sum holds v after an add)."""
         layer, s = self.layer, self.layer.shape
         layer._check_gate(seq_len)
+        self._check_shapes(x, add, shared_w)
         if keep_gu and isinstance(layer, Int8MoELayer):
             raise ValueError("keep_gu is for the backward, which an Int8MoELayer does not have")
         T = x.shape[0]
@@ -875,18 +886,22 @@ class MoEBlock:
         """Backward for the output gradient dy (x's type) after a forward of x
         (with the same shared_w and seq_len).  Returns (the block's buffers, the
         layer's backward buffers): dx - the gradient of x and of add alike -,
-        d_weight, d_post_weight (with a post_norm or post_weight) and d_shared_w
-        (with shared_w); dC, dW_gu, dW_dn, dw of the layer."""
+        d_weight (with a weight), d_post_weight (with a post_weight) and
+        d_shared_w (with shared_w); dC, dW_gu, dW_dn, dw of the layer."""
         layer, s = self.layer, self.layer.shape
         if isinstance(layer, Int8MoELayer):
             layer.backward()
         layer._check_backward(seq_len)
         if dy.dtype != x.dtype or dy.shape != x.shape:
             raise ValueError(f"dy {tuple(dy.shape)} {dy.dtype} and x {tuple(x.shape)} {x.dtype} differ")
+        self._check_shapes(x, None, shared_w)
         T = dy.shape[0]
-        f, b, bb = self.buffers(T, dy.dtype).gradients(), layer.buffers(T), layer.backward_buffers(T)
+        f = self.buffers(T, dy.dtype)
+        if f.added is None:
+            raise ValueError(f"backward of {T} tokens in {dy.dtype} before a forward of them")
         if T and not f.added and x.data_ptr() == f.y.data_ptr():
             raise ValueError("x is the block's own y, which the forward has written over: pass a copy of it to both")
+        f, b, bb = f.gradients(), layer.buffers(T), layer.backward_buffers(T)
         st = stream if stream is not None else torch.cuda.current_stream()
         weighted = self.post_weight is not None
         L.moe_combine_norm_backward(

@@ -198,3 +198,15 @@ def test_block_on_its_own_output():
     blk = M.MoEBlock(build(M.Int8MoELayer, synth.CONFIGS["mid"], None)[0])
     with pytest.raises(ValueError, match="keep_gu"):
         blk.forward(torch.zeros((4, synth.CONFIGS["mid"].H), device="cuda"), keep_gu=True)
+
+
+def test_block_refuses_wrong_shapes():
+    cfg = synth.CONFIGS["tiny"]
+    layer = bf16_layer(cfg)[0]
+    x, w = (torch.zeros(s, device="cuda") for s in ((cfg.T, cfg.H), (cfg.T,)))
+    block = M.MoEBlock(layer)
+    for bad in (lambda: M.MoEBlock(layer, x), lambda: M.MoEBlock(layer, None, EPS, True, x[0, 8:]),
+                lambda: block.forward(x[:, 8:]), lambda: block.forward(x, x[1:].bfloat16()),
+                lambda: block.forward(x, None, w[1:]), lambda: block.backward(x, x, w[1:]), lambda: block.backward(x, x)):
+        with pytest.raises(ValueError):
+            bad()
