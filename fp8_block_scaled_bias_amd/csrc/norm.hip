@@ -10,6 +10,12 @@
 // backward passes run a fixed number of workgroups over the tokens, each with
 // its part of the weight's gradient in registers; the parts are added up, in
 // order, by a second launch.
+//
+// 16384 x 7168 (HBM reads 6.05, copies 4.7 TB/s): norm of fp32 with the add and
+// E4M3 codes 265 us (5.8 TB/s), its gradient in bf16 184 us (5.1); combine of 8
+// rows and the shared one with norm 474 us (5.4), its gradient with codes 1290
+// us (4.3).  128 rows: 4.9 us, a launch and one row's chain of steps; the weight
+// loaded ahead of the sums gains nothing there and costs 4 % at 16384.
 #include "gemm_common.h"
 
 namespace moe {
