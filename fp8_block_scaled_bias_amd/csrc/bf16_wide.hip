@@ -131,7 +131,7 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
   const int xcd = blockIdx.x & 7, jw = blockIdx.x >> 3, nper = gridDim.x >> 3;
   int64_t tlo, thi;
   if (PT) {
-    constexpr int OVER = 3;  // a tile's stores, in K blocks (65 groups: 2 to 4 4.35 ms, 8 4.77, 12 5.08)
+    constexpr int OVER = 3;  // a tile's stores, in K blocks (65 groups: 1 4.37, 2 4.10, 3 4.00, 5 4.14 ms)
     const int64_t per = mtiles * ntiles, cost = s_pref[G] + (int64_t)OVER * G;
     auto cut = [&](int x) -> int64_t {  // first tile of XCD x
       const int64_t c = cost * x;       // in eighths
