@@ -22,6 +22,7 @@ using gemm::build_group_tables;
 using gemm::dma16;
 using gemm::MAXG;
 using gemm::swz;
+using gemm::wait_copies;
 
 constexpr int MT = 256;
 constexpr int BM = 128, BN = 128;
@@ -29,12 +30,6 @@ constexpr int S = 4;                  // stages
 constexpr int REG = 128 * 128;        // an operand's K block
 constexpr int STAGE = 2 * REG;
 constexpr int COPIES = 4;             // of a wave, operand and K block
-
-// s_waitcnt vmcnt(N) lgkmcnt(0)
-template <int N>
-__device__ __forceinline__ void wait_copies() {
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
-}
 
 template <int MODE>
 __global__ __launch_bounds__(MT, 1) void mid_kernel(Args a) {

@@ -40,8 +40,11 @@ namespace {
 
 using gemm::barrier;
 using gemm::build_group_tables;
+using gemm::copy4;
+using gemm::load_rsrc;
 using gemm::MAXG;
 using gemm::swz;
+using gemm::wait_copies;
 
 constexpr int WT = 256;
 constexpr int REG = 128 * 128;      // a region: 16 KB
@@ -56,34 +59,16 @@ static_assert((MAXG + 1) * 4 <= 4112 && LDS <= 160 * 1024 - 256, "LDS budget");
 template <int V>
 using ic = std::integral_constant<int, V>;
 
-__device__ __forceinline__ v4i rsrc(const void* p, uint32_t bytes) {
-  const uint64_t a = reinterpret_cast<uint64_t>(p);
-  v4i r;
-  r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
-  r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
-  r[2] = __builtin_amdgcn_readfirstlane((int)bytes);
-  r[3] = 0x00020000;
-  return r;
-}
-// Lane i's 16 (4) bytes from offset voff + soff of the resource land at m0 +
-// i * 16 (4); out of range: not read from memory.
-// (resources that change with the K block may have been put into vector
-// registers: taken back where they were, nothing where they were not)
-__device__ __forceinline__ void copy16(const v4i& d, uint32_t voff, uint32_t soff, uint32_t m0) {
+// Resources that change with the K block may have been put into vector registers:
+// taken back where they were (FRESH: as in the weight gradient of gathered rows,
+// between the load and which there have to be wait states).
+template <bool FRESH>
+__device__ __forceinline__ void copy_block16(const v4i& d, uint32_t voff, uint32_t soff, uint32_t m0) {
   v4i r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) r[i] = __builtin_amdgcn_readfirstlane(d[i]);
-  asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-               ::"v"(voff), "s"(r), "s"(soff), "s"(m0) : "memory", "m0");
-}
-__device__ __forceinline__ void copy4(const v4i& r, uint32_t voff, uint32_t m0) {
-  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dword %0, %1, 0 offen lds"
-               ::"v"(voff), "s"(r), "s"(m0) : "memory", "m0");
-}
-// s_waitcnt vmcnt(N) lgkmcnt(0)
-template <int N>
-__device__ __forceinline__ void wait_copies() {
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+  if (FRESH) gemm::copy16_fresh(r, voff, soff, m0);
+  else gemm::copy16(r, voff, soff, m0);
 }
 
 __device__ __forceinline__ int64_t uniform(int64_t v) {
@@ -241,7 +226,7 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
   // kGlu, kPlain: the row indices of a tile into slot o % 4.  kWgrad: those of
   // a K block of 64 rows into the wave's own slot, counted over all blocks.
   auto index_copy = [&](const Tile& t, int o) {
-    copy4(rsrc(a.index + t.m0, (uint32_t)t.rows * 4), (uint32_t)(64 * wv + lane) * 4,
+    copy4(load_rsrc(a.index + t.m0, (uint32_t)t.rows * 4), (uint32_t)(64 * wv + lane) * 4,
           (uint32_t)__builtin_amdgcn_readfirstlane((int)(lds0 + OFF_IDX + (o & 3) * 1024 + wv * 256)));
   };
   auto index_of = [&](int o, int row) -> uint32_t {
@@ -259,7 +244,7 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
   auto index_block = [&]() {
     const int64_t r0 = (int64_t)x_k0 + 64 * xk;
     const int left = min(64, x_kc - 64 * xk);
-    copy4(rsrc(a.index + (left > 0 ? r0 : 0), (uint32_t)max(left, 1) * 4), (uint32_t)lane * 4,
+    copy4(load_rsrc(a.index + (left > 0 ? r0 : 0), (uint32_t)max(left, 1) * 4), (uint32_t)lane * 4,
           (uint32_t)__builtin_amdgcn_readfirstlane((int)(lds0 + OFF_IDX + wv * 1024 + (xb & 3) * 256)));
     ++xb;
     if (++xk == max(2, (x_kc + 63) >> 6)) {
@@ -277,11 +262,11 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
       for (int h = 0; h < 2; ++h) {
         // (a half without columns copies the other's)
         const int cols = min(128, ct.rows - 128 * h), hh = cols > 0 ? h : 0;
-        rp[PT ? h : 0] = rsrc(a.P + row * a.N + ct.m0 + 128 * hh,
+        rp[PT ? h : 0] = load_rsrc(a.P + row * a.N + ct.m0 + 128 * hh,
                               (uint32_t)(left - 1) * ldp + 2u * (uint32_t)(cols > 0 ? cols : min(128, ct.rows)));
         const int qc = cols_of(ct, h), qh = qc > 0 ? h : 0;
         if (!GATHER)
-          rq[h] = rsrc(a.Q + row * a.K + ct.n0 + 128 * qh,
+          rq[h] = load_rsrc(a.Q + row * a.K + ct.n0 + 128 * qh,
                        (uint32_t)(left - 1) * ldq + 2u * (uint32_t)(qc > 0 ? qc : cols_of(ct, 0)));
       }
       if (GATHER) {
@@ -297,7 +282,7 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int qc = cols_of(ct, h), qh = qc > 0 ? h : 0;
-        rq[h] = rsrc(a.Q + ((int64_t)ct.g * q_rows + (ct.kc > 64 * ck ? 64 * ck : 0)) * a.K + ct.n0 + 128 * qh,
+        rq[h] = load_rsrc(a.Q + ((int64_t)ct.g * q_rows + (ct.kc > 64 * ck ? 64 * ck : 0)) * a.K + ct.n0 + 128 * qh,
                      (uint32_t)(left - 1) * ldq + 2u * (uint32_t)(qc > 0 ? qc : cols_of(ct, 0)));
       }
     }
@@ -311,7 +296,7 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
       for (int h = 0; h < 2; ++h) {
         const int hh = h && cols_of(ct, 1) > 0;
         const int64_t row = (int64_t)ct.g * q_rows + ct.n0 + (GLU ? h * a.N : hh * 128);
-        rq[h] = rsrc(a.Q + row * a.K, (uint32_t)cols_of(ct, hh) * ldq);
+        rq[h] = load_rsrc(a.Q + row * a.K, (uint32_t)cols_of(ct, hh) * ldq);
       }
     }
     if (PT) {
@@ -320,10 +305,10 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
         for (int h = 0; h < 2; ++h) {
           const int qc = cols_of(ct, h), qh = qc > 0 ? h : 0;
           const int64_t at = ct.n0 + 128 * qh;
-          rq[h] = rsrc(a.Q + at, (uint32_t)a_last * ldq + 2u * (uint32_t)(qc > 0 ? qc : cols_of(ct, 0)));
+          rq[h] = load_rsrc(a.Q + at, (uint32_t)a_last * ldq + 2u * (uint32_t)(qc > 0 ? qc : cols_of(ct, 0)));
         }
     } else if (GATHER) {
-      rp[0] = rsrc(a.P, (uint32_t)a.A_rows * ldp);
+      rp[0] = load_rsrc(a.P, (uint32_t)a.A_rows * ldp);
       // (the lane's place passes through an empty asm so that what follows
       // is computed here and not kept in registers over the K loop)
       int ln = lane;
@@ -335,7 +320,7 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
       }
       index_copy(cn, co + 1);
     } else {
-      rp[0] = rsrc(a.P + (int64_t)ct.m0 * (ldp / 2), (uint32_t)ct.rows * ldp);
+      rp[0] = load_rsrc(a.P + (int64_t)ct.m0 * (ldp / 2), (uint32_t)ct.rows * ldp);
     }
     aim_block();
   };
@@ -345,10 +330,10 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
     const uint32_t m = m0_w + st * STAGE + R * REG + C * 1024;
     if (R >= 2) {
       const bool past = !QT && (ck * 64 >= ct.kc || (ck == ct.nkb - 1 && cut_q[C & 1]));
-      copy16(rq[R & 1], past ? kOut : vq[C], QT ? 0 : (uint32_t)ck * 128, m);
+      copy_block16<PT && GATHER>(rq[R & 1], past ? kOut : vq[C], QT ? 0 : (uint32_t)ck * 128, m);
     } else {
       const bool past = !PT && (ck * 64 >= ct.kc || (ck == ct.nkb - 1 && cut_p[C & 1]));
-      copy16(rp[PT ? R & 1 : 0], past ? kOut : vp[PT ? C : (4 * R + C) & 7], PT ? 0 : (uint32_t)ck * 128, m);
+      copy_block16<PT && GATHER>(rp[PT ? R & 1 : 0], past ? kOut : vp[PT ? C : (4 * R + C) & 7], PT ? 0 : (uint32_t)ck * 128, m);
     }
   };
   auto copy_region = [&](auto R_, uint32_t st) __attribute__((always_inline)) {

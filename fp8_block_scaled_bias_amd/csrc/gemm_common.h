@@ -10,6 +10,7 @@
 #pragma once
 
 #include "common.h"
+#include "lds_copy.h"
 
 namespace moe {
 namespace gemm {
@@ -61,21 +62,6 @@ __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-}
-
-// Asynchronous global -> LDS copies.  Lane i's bytes land at lds + i*size;
-// lds must be wave-uniform.  No VGPR is written.
-// (lds is made wave-uniform explicitly: inside branches the compiler cannot
-// always prove it.)
-__device__ __forceinline__ void dma16(const void* g, uint32_t lds) {
-  const uint32_t l = __builtin_amdgcn_readfirstlane(lds);
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(l)
-               : "memory", "m0");
-}
-__device__ __forceinline__ void dma4(const void* g, uint32_t lds) {
-  const uint32_t l = __builtin_amdgcn_readfirstlane(lds);
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(l)
-               : "memory", "m0");
 }
 
 // One 16x16 output block over one 128-wide K block: lane l supplies 32 bytes

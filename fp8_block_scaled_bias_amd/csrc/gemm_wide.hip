@@ -53,7 +53,6 @@ namespace gemm {
 namespace {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
-typedef int v4i __attribute__((ext_vector_type(4)));
 
 constexpr int WT = 512;                  // 8 waves, 2 per SIMD
 constexpr int WBM = 256;                 // tile rows
@@ -85,40 +84,6 @@ __device__ __forceinline__ v16f mfma32(const v8i& x, const v8i& y, const v16f& c
 // of an address is one VGPR, the rest an SGPR offset.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t out_rsrc(const void* p, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
-}
-
-// The same descriptor as four SGPRs, for the copies below (stride 0: the
-// range check is offset < bytes; loads past it return zeros).
-__device__ __forceinline__ v4i load_rsrc(const void* p, uint32_t bytes) {
-  const uint64_t a = reinterpret_cast<uint64_t>(p);
-  v4i r;
-  r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
-  r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
-  r[2] = __builtin_amdgcn_readfirstlane((int)bytes);
-  r[3] = 0x00020000;
-  return r;
-}
-
-// Asynchronous copies into LDS.  Lane i's 16 (4) bytes come from buffer
-// offset voff + soff and land at m0 + i*16 (i*4); soff moves the global
-// address only.  m0 and soff must be wave-uniform (SGPRs).
-template <int IMM>
-__device__ __forceinline__ void copy16(const v4i& r, uint32_t voff, uint32_t soff, uint32_t m0b) {
-  asm volatile("s_add_u32 m0, %3, %4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-               ::"v"(voff), "s"(r), "s"(soff), "s"(m0b), "n"(IMM)
-               : "memory", "m0", "scc");
-}
-__device__ __forceinline__ void copy4(const v4i& r, uint32_t voff, uint32_t soff, uint32_t m0) {
-  asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dword %0, %1, %2 offen lds"
-               ::"v"(voff), "s"(r), "s"(soff), "s"(m0)
-               : "memory", "m0");
-}
-
-// s_waitcnt vmcnt(N) lgkmcnt(0)
-template <int N>
-__device__ __forceinline__ void wait_vmcnt_lgkm0() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
 }
 
 template <int V>
@@ -333,10 +298,7 @@ __global__ __launch_bounds__(WT, 1) void wide_gemm_kernel(GemmArgs args) {
     return (uint32_t)__builtin_amdgcn_readfirstlane(
         (int)(lds0 + OFF_RIDX + (uint32_t)(((ord & 3) * 256 + 64 * (wv & 3)) * 4)));
   };
-  auto table_copy = [&](const int32_t* src, uint32_t m0) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(m0)
-                 : "memory", "m0");
-  };
+  auto table_copy = [&](const int32_t* src, uint32_t m0) { dma4(src, m0); };
   // LDS destinations: this wave's first tile-copy row, its scale slice
   const uint32_t m0_w =
       (uint32_t)__builtin_amdgcn_readfirstlane((int)(lds0 + (uint32_t)(32 * wv) * 128));
@@ -622,7 +584,7 @@ __global__ __launch_bounds__(WT, 1) void wide_gemm_kernel(GemmArgs args) {
       // not)
       if ((U & 1) == 1) {
         if (PH == 0 && U == 1) wait_vm_lgkm0();
-        else wait_vmcnt_lgkm0<NS>();
+        else wait_copies<NS>();
         barrier();
         read_ops(ic<(U == 1 ? 1 : 0)>(), ic<0>());
       }

@@ -14,8 +14,11 @@ namespace {
 
 using gemm::barrier;
 using gemm::build_group_tables;
+using gemm::copy16;
+using gemm::load_rsrc;
 using gemm::MAXG;
 using gemm::swz;
+using gemm::wait_copies;
 
 constexpr int MT = 256;
 constexpr int BM = 128, BN = 128;
@@ -23,26 +26,6 @@ constexpr int S = 4;                           // stages
 constexpr int STAGE = (BM + BN) * 128;
 constexpr int AC = BM / 32, BC = BN / 32;      // copies of a wave and K block
 constexpr int MI = BM / 64;                    // row blocks of a wave
-
-__device__ __forceinline__ v4i rsrc(const void* p, uint32_t bytes) {
-  const uint64_t a = reinterpret_cast<uint64_t>(p);
-  v4i r;
-  r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
-  r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
-  r[2] = __builtin_amdgcn_readfirstlane((int)bytes);
-  r[3] = 0x00020000;
-  return r;
-}
-// Lane i's 16 bytes from offset voff + soff of the resource land at m0 + 16 i;
-// out of range: not read from memory.
-__device__ __forceinline__ void copy16(const v4i& r, uint32_t voff, uint32_t soff, uint32_t m0) {
-  asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-               ::"v"(voff), "s"(r), "s"(soff), "s"(m0) : "memory", "m0");
-}
-template <int N>
-__device__ __forceinline__ void wait_copies() {
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
-}
 
 template <bool SWIGLU>
 __global__ __launch_bounds__(MT, 1) void mid_kernel(Args a) {
@@ -100,8 +83,8 @@ __global__ __launch_bounds__(MT, 1) void mid_kernel(Args a) {
   auto aim = [&]() {
     const Place p = place(co);
     const int64_t cols = N - p.n0 < TN ? N - p.n0 : TN;
-    rb = rsrc(a.B + ((int64_t)p.g * b_rows + (SWIGLU && wv >= 2 ? N : 0) + p.n0) * K, (uint32_t)(cols * K));
-    ra = a.index ? rsrc(a.A, (uint32_t)a.A_rows * K) : rsrc(a.A + (int64_t)p.m0 * K, (uint32_t)p.rows * K);
+    rb = load_rsrc(a.B + ((int64_t)p.g * b_rows + (SWIGLU && wv >= 2 ? N : 0) + p.n0) * K, (uint32_t)(cols * K));
+    ra = a.index ? load_rsrc(a.A, (uint32_t)a.A_rows * K) : load_rsrc(a.A + (int64_t)p.m0 * K, (uint32_t)p.rows * K);
 #pragma unroll
     for (int c = 0; c < BC; ++c) {
       const int row = 32 * wv + 8 * c + (lane >> 3);

@@ -46,8 +46,12 @@ namespace {
 
 using gemm::barrier;
 using gemm::build_group_tables;
+using gemm::copy16;
+using gemm::copy4;
+using gemm::load_rsrc;
 using gemm::MAXG;
 using gemm::swz;
+using gemm::wait_copies;
 
 constexpr int WT = 256;
 constexpr int REG = 128 * 128;      // a region: 128 rows x 128 B
@@ -63,31 +67,6 @@ static_assert((MAXG + 1) * 4 <= 4112 && LDS <= 160 * 1024 - 256, "LDS budget");
 
 template <int V>
 using ic = std::integral_constant<int, V>;
-
-__device__ __forceinline__ v4i rsrc(const void* p, uint32_t bytes) {
-  const uint64_t a = reinterpret_cast<uint64_t>(p);
-  v4i r;
-  r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
-  r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
-  r[2] = __builtin_amdgcn_readfirstlane((int)bytes);
-  r[3] = 0x00020000;
-  return r;
-}
-// Lane i's 16 (4) bytes from offset voff + soff of the resource land at m0 +
-// i * 16 (4); out of range: not read from memory.
-__device__ __forceinline__ void copy16(const v4i& r, uint32_t voff, uint32_t soff, uint32_t m0) {
-  asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-               ::"v"(voff), "s"(r), "s"(soff), "s"(m0) : "memory", "m0");
-}
-__device__ __forceinline__ void copy4(const v4i& r, uint32_t voff, uint32_t m0) {
-  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dword %0, %1, 0 offen lds"
-               ::"v"(voff), "s"(r), "s"(m0) : "memory", "m0");
-}
-// s_waitcnt vmcnt(N) lgkmcnt(0)
-template <int N>
-__device__ __forceinline__ void wait_copies() {
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
-}
 
 struct Tile {
   int g, n0, m0, rows;
@@ -167,7 +146,7 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
   int co = 0, ck = 0, cg = 0;
   v4i ra, rb[2];
   auto index_copy = [&](const Tile& t, int o) {  // the row indices of a tile into slot o & 3
-    copy4(rsrc(a.index + t.m0, (uint32_t)t.rows * 4), (uint32_t)(64 * wv + lane) * 4,
+    copy4(load_rsrc(a.index + t.m0, (uint32_t)t.rows * 4), (uint32_t)(64 * wv + lane) * 4,
           (uint32_t)__builtin_amdgcn_readfirstlane((int)(lds0 + OFF_IDX + (o & 3) * 1024 + wv * 256)));
   };
   auto index_of = [&](int o, int row) -> uint32_t {
@@ -180,10 +159,10 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
       // (a half without columns copies the other's rows; K offsets never lie
       // past a resource's end)
       const int hh = h && cols_of(t, 1) > 0;
-      rb[h] = rsrc(a.B + ((int64_t)t.g * b_rows + t.n0 + hh * b_half) * K, (uint32_t)cols_of(t, hh) * K);
+      rb[h] = load_rsrc(a.B + ((int64_t)t.g * b_rows + t.n0 + hh * b_half) * K, (uint32_t)cols_of(t, hh) * K);
     }
     if (GATHER) {
-      ra = rsrc(a.A, (uint32_t)a.A_rows * K);
+      ra = load_rsrc(a.A, (uint32_t)a.A_rows * K);
       // (the lane's place passes through an empty asm so that what follows
       // is computed here and not kept in registers over the K loop)
       int ln = lane;
@@ -196,7 +175,7 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
       int g2 = cg;
       index_copy(tile_at(g2, co + 1), co + 1);
     } else {
-      ra = rsrc(a.A + (int64_t)t.m0 * K, (uint32_t)t.rows * K);
+      ra = load_rsrc(a.A + (int64_t)t.m0 * K, (uint32_t)t.rows * K);
     }
   };
   // copy c of region R (0, 1: A0, A1; 2, 3: B0, B1) of K block ck into stage st
@@ -255,11 +234,11 @@ __global__ __launch_bounds__(WT, 1) void wide_kernel(Args a) {
     asm volatile("" : "+v"(ln));
     const int row = 64 * wv + ln;
     if (GATHER)
-      copy4(rsrc(a.sa, (uint32_t)a.A_rows * 4), row < t.rows ? index_of(to, row) * 4 : kOut, m);
+      copy4(load_rsrc(a.sa, (uint32_t)a.A_rows * 4), row < t.rows ? index_of(to, row) * 4 : kOut, m);
     else
-      copy4(rsrc(a.sa + t.m0, (uint32_t)t.rows * 4), (uint32_t)row * 4, m);
+      copy4(load_rsrc(a.sa + t.m0, (uint32_t)t.rows * 4), (uint32_t)row * 4, m);
     const int h = wv >> 1;
-    copy4(rsrc(a.sb + (int64_t)t.g * b_rows + t.n0 + h * b_half, (uint32_t)cols_of(t, h) * 4),
+    copy4(load_rsrc(a.sb + (int64_t)t.g * b_rows + t.n0 + h * b_half, (uint32_t)cols_of(t, h) * 4),
           (uint32_t)(64 * (wv & 1) + ln) * 4, m + 1024);
   };
 

@@ -29,6 +29,7 @@
 //  3. bias_update: the +-gamma rule on the counts.
 //  4. sum_partials: the logits themselves, for the gate of gate.hip.
 #include "common.h"
+#include "lds_copy.h"
 
 namespace moe {
 namespace {
@@ -157,28 +158,8 @@ constexpr int RW_PB = 256 * 64;            // one plane's stage
 constexpr int RW_STAGE = RW_XB + 3 * RW_PB;
 
 typedef float v16f_r __attribute__((ext_vector_type(16)));
-typedef int v4i_r __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ int rw_swz(int row) { return ((row >> 1) & 3) ^ ((row >> 3) & 1); }
-
-__device__ __forceinline__ v4i_r rw_rsrc(const void* p, uint32_t bytes) {
-  const uint64_t a = reinterpret_cast<uint64_t>(p);
-  v4i_r r;
-  r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
-  r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
-  r[2] = __builtin_amdgcn_readfirstlane((int)bytes);
-  r[3] = 0x00020000;
-  return r;
-}
-
-// Lane i's 16 bytes from buffer offset voff + soff land at m0 + IMM + i*16
-// (soff moves the global address only; loads past the buffer return 0).
-template <int IMM>
-__device__ __forceinline__ void rw_copy(const v4i_r& r, uint32_t voff, uint32_t soff, uint32_t m0b) {
-  asm volatile("s_add_u32 m0, %3, %4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-               ::"v"(voff), "s"(r), "s"(soff), "s"(m0b), "n"(IMM)
-               : "memory", "m0", "scc");
-}
 
 __global__ void split_planes_kernel(const float* __restrict__ C, int64_t n,
                                     uint16_t* __restrict__ planes) {
@@ -210,16 +191,16 @@ __global__ __launch_bounds__(512, 1) void router_logits_wide_kernel(
   // +lane/4, LDS slot lane%4 <- global chunk (lane%4) ^ rw_swz(row)
   const int rl = 128 * (wv & 1) + (lane >> 2);
   const uint32_t gch = (uint32_t)((lane & 3) ^ rw_swz(rl));
-  v4i_r rs;
+  gemm::v4i rs;
   uint32_t voff;
   uint32_t region;
   if (wv < 2) {
-    rs = rw_rsrc(x, (uint32_t)T * rowb);
+    rs = gemm::load_rsrc(x, (uint32_t)T * rowb);
     voff = (uint32_t)(tok0 + rl) * rowb + gch * 16;
     region = 0;
   } else {
     const int pl = (wv - 2) >> 1;
-    rs = rw_rsrc(planes, 3u * (uint32_t)E * rowb);
+    rs = gemm::load_rsrc(planes, 3u * (uint32_t)E * rowb);
     voff = (uint32_t)(pl * E + rl) * rowb + gch * 16;
     region = RW_XB + pl * RW_PB;
   }
@@ -229,14 +210,14 @@ __global__ __launch_bounds__(512, 1) void router_logits_wide_kernel(
   auto copy_step = [&](auto ST_, int st) __attribute__((always_inline)) {
     constexpr int ST = decltype(ST_)::value;
     const uint32_t so = (uint32_t)(k0 + 32 * st) * 2;
-    rw_copy<ST * RW_STAGE + 0 * 1024>(rs, voff, so, m0b);
-    rw_copy<ST * RW_STAGE + 1 * 1024>(rs, voff, so + s16, m0b);
-    rw_copy<ST * RW_STAGE + 2 * 1024>(rs, voff, so + 2 * s16, m0b);
-    rw_copy<ST * RW_STAGE + 3 * 1024>(rs, voff, so + 3 * s16, m0b);
-    rw_copy<ST * RW_STAGE + 4 * 1024>(rs, voff, so + 4 * s16, m0b);
-    rw_copy<ST * RW_STAGE + 5 * 1024>(rs, voff, so + 5 * s16, m0b);
-    rw_copy<ST * RW_STAGE + 6 * 1024>(rs, voff, so + 6 * s16, m0b);
-    rw_copy<ST * RW_STAGE + 7 * 1024>(rs, voff, so + 7 * s16, m0b);
+    gemm::copy16<ST * RW_STAGE + 0 * 1024>(rs, voff, so, m0b);
+    gemm::copy16<ST * RW_STAGE + 1 * 1024>(rs, voff, so + s16, m0b);
+    gemm::copy16<ST * RW_STAGE + 2 * 1024>(rs, voff, so + 2 * s16, m0b);
+    gemm::copy16<ST * RW_STAGE + 3 * 1024>(rs, voff, so + 3 * s16, m0b);
+    gemm::copy16<ST * RW_STAGE + 4 * 1024>(rs, voff, so + 4 * s16, m0b);
+    gemm::copy16<ST * RW_STAGE + 5 * 1024>(rs, voff, so + 5 * s16, m0b);
+    gemm::copy16<ST * RW_STAGE + 6 * 1024>(rs, voff, so + 6 * s16, m0b);
+    gemm::copy16<ST * RW_STAGE + 7 * 1024>(rs, voff, so + 7 * s16, m0b);
   };
 
   v16f_r acc[2][4];
