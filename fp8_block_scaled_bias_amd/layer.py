@@ -116,8 +116,31 @@ class Gate:
     scale: float = 1.0
 
 
+@dataclasses.dataclass(frozen=True)
+class Held:
+    """Which forward a layer's buffers hold, as far as its backward has to know:
+    whether the gate and up outputs were kept, the balance statistic's seq_len;
+    of a MoEBlock its own buffers, whether it had an add and a shared_w."""
+    gu: bool
+    seq_len: int | None = None
+    block: object = None
+    added: bool = False
+    gated: bool = False
+
+
+class CapturedForward(torch.cuda.CUDAGraph):
+    """The graph of one forward.  A replay leaves its buffers as that forward
+    does, whichever was called in between, and they are noted as such."""
+    bufs = held = None
+
+    def replay(self):
+        super().replay()
+        self.bufs.held = self.held
+
+
 class Buffers:
-    """Device buffers of one forward at T tokens (reused across calls)."""
+    """Device buffers of one forward at T tokens (reused across calls).  held:
+    the forward that they hold, None before the first."""
 
     def __init__(self, shape: LayerShape, T: int, device="cuda"):
         s = shape
@@ -125,6 +148,7 @@ class Buffers:
         dev = torch.device(device)
         u8, i32, f32, bf = torch.uint8, torch.int32, torch.float32, torch.bfloat16
         self.T, self.R = T, R
+        self.held = None
         self.topk_idx = torch.empty((T, s.k), dtype=i32, device=dev)
         self.topk_w = torch.empty((T, s.k), dtype=f32, device=dev)
         self.topk_s = torch.empty((T, s.k), dtype=f32, device=dev)   # the chosen experts' scores
@@ -364,6 +388,7 @@ class MoELayer:
             e1.record(on)
             events.setdefault(name, []).append((e0, e1))
 
+        b.held = None
         side.wait_stream(st)
         step("quant", side, lambda: self._quantise(x_bf16, b, side))
         step("route", st, lambda: self._route(x_bf16, b, seq_len, st))
@@ -377,6 +402,7 @@ class MoELayer:
                                                   s.H, b.y, st))
         if update_bias:
             step("bias", st, lambda: L.moe_bias_update(b.counts, self.bias, s.E, gamma, st))
+        b.held = Held(keep_gu, seq_len)
         return b.y
 
     def _quantise(self, x_bf16, b, stream):
@@ -392,7 +418,6 @@ class MoELayer:
     def _experts(self, x_bf16, b, keep_gu, st, step):
         """The experts' rows b.d of the operand and the permutation in b."""
         s, R = self.shape, b.R
-        b.gu_kept = keep_gu
         if keep_gu:
             step("gate_up", st, lambda: L.grouped_fp8_gemm_swiglu_keep(
                 b.xq, b.xs, b.perm_src, self.w_gu, self.w_gu_s, b.offsets, s.G, R, s.I, s.H,
@@ -417,7 +442,8 @@ class MoELayer:
         replay() reruns the whole layer on the same buffers - write the next
         batch into x_bf16 first - with one launch.  The library only launches
         kernels (no allocation, no memset, no host synchronisation), so every
-        step is capturable.  forward_kw as in forward (not events)."""
+        step is capturable.  forward_kw as in forward (not events).  A backward
+        that is called after a replay is that of the captured forward."""
         T = x_bf16.shape[0]
         b = bufs or self.buffers(T)
         side = torch.cuda.Stream()   # default priority
@@ -426,9 +452,10 @@ class MoELayer:
             self.forward(x_bf16, b, stream=side, **forward_kw)   # warm-up outside the capture
         torch.cuda.current_stream().wait_stream(side)
         torch.cuda.synchronize()
-        graph = torch.cuda.CUDAGraph()
+        graph = CapturedForward()
         with torch.cuda.graph(graph):
             self.forward(x_bf16, b, stream=torch.cuda.current_stream(), **forward_kw)
+        graph.bufs, graph.held = b, b.held
         return graph
 
     def backward_buffers(self, T: int) -> BackwardBuffers:
@@ -459,6 +486,7 @@ class MoELayer:
         s = self.shape
         T = dy_bf16.shape[0]
         b = bufs or self.buffers(T)
+        self._check_seq_len(b, seq_len)
         bb = bwd or self.backward_buffers(T)
         if keep_intermediates:
             bb.intermediates()
@@ -491,7 +519,7 @@ class MoELayer:
         R, G, H, I, k, cap = b.R, s.G, s.H, s.I, s.k, bb.cap
         step("dgrad_down", lambda: L.grouped_fp8_gemm_dgrad(
             bb.dDq, bb.dDs, self.w_dn, self.w_dn_s, b.offsets, G, R, H, I, bb.dh, st))
-        if getattr(b, "gu_kept", False):
+        if b.held is not None and b.held.gu:
             gu = b.hgu   # kept by the forward (keep_gu): the same bf16 GEMM output
         else:
             gu = bb.gu
@@ -543,8 +571,6 @@ class MoELayer:
                 L.moe_router_dcentroids(x_bf16, b.perm_src, b.offsets, bb.dlogit_rows, T, H, s.E,
                                         bb.dC, st)))
         else:
-            if getattr(b, "_seq_len", None) != seq_len:
-                raise ValueError("backward with seq_len needs the forward run with the same seq_len")
             bb.dense()
             step("router_bwd", lambda: L.moe_router_backward_dense(
                 x_bf16, self.centroids, b.topk_idx, bb.dw, b.scores, b.score_sums, b.seq_f, T, H,
@@ -555,6 +581,11 @@ class MoELayer:
         self._check_gate(seq_len)
         if self.gate is not None and self.shape.E % 16:
             raise ValueError(f"the backward of a layer with a Gate needs E % 16 == 0, E is {self.shape.E}")
+
+    @staticmethod
+    def _check_seq_len(b, seq_len):
+        if seq_len is not None and (b.held is None or b.held.seq_len != seq_len):
+            raise ValueError("backward with seq_len needs the forward run with the same seq_len")
 
     def _check_gate(self, seq_len):
         """What a layer with a Gate does not do, before anything is launched."""
@@ -641,6 +672,7 @@ class Int8MoELayer(MoELayer):
         if self._side is None:
             self._side = torch.cuda.Stream(device=st.device)
         side = self._side
+        b.held = None
         side.wait_stream(st)
         self._quantise(x_bf16, b, side)
         self._route(x_bf16, b, None, st)
@@ -651,6 +683,7 @@ class Int8MoELayer(MoELayer):
         L.moe_combine(b.d, b.inv_perm, b.topk_w, shared, T, s.k, s.H, b.y, st)
         if update_bias:
             L.moe_bias_update(b.counts, self.bias, s.E, gamma, st)
+        b.held = Held(False)
         return b.y
 
     def _quantise(self, x_bf16, b, stream):
@@ -751,7 +784,6 @@ class Bf16MoELayer(MoELayer):
 
     def _experts(self, x_bf16, b, keep_gu, st, step):
         s, R = self.shape, b.R
-        b.gu_kept = keep_gu
         step("gate_up", st, lambda: L.grouped_bf16_gemm_glu(
             x_bf16, b.perm_src, self.w_gu, b.offsets, s.G, R, s.I, s.H, self.act, b.h,
             b.hgu if keep_gu else None, st))
@@ -761,7 +793,7 @@ class Bf16MoELayer(MoELayer):
     def _experts_backward(self, x_bf16, b, bb, keep_intermediates, st, step):
         s = self.shape
         R, G, H, I = b.R, s.G, s.H, s.I
-        if getattr(b, "gu_kept", False):
+        if b.held is not None and b.held.gu:
             gu = b.hgu
         else:
             gu = bb.gu
@@ -789,7 +821,6 @@ class BlockBuffers:
         self.n = torch.empty((T, shape.H), dtype=torch.bfloat16, device=dev)
         self.rstd = torch.empty((T,), dtype=f32, device=dev)
         self.y = torch.empty((T, shape.H), dtype=dtype, device=dev)
-        self.added = None   # (True or False after a forward)
         self._sum = self.dx = None
 
     @property
@@ -864,10 +895,10 @@ class MoEBlock:
         T = x.shape[0]
         f, b = self.buffers(T, x.dtype), layer.buffers(T)
         st = stream if stream is not None else torch.cuda.current_stream()
-        f.added = add is not None
-        v = f.sum if f.added else x
+        b.held = None
+        v = f.sum if add is not None else x
         codes, scales = (None, None) if layer.CODES == L.QUANT_NONE else (b.xq, b.xs)
-        L.moe_norm(x, add, self.weight, T, s.H, self.eps, v if f.added else None, f.n, f.rstd, layer.CODES,
+        L.moe_norm(x, add, self.weight, T, s.H, self.eps, None if add is None else v, f.n, f.rstd, layer.CODES,
                    codes, scales, st)
         layer._route(f.n, b, seq_len, st)
         if seq_len is not None:
@@ -879,12 +910,16 @@ class MoEBlock:
                            self.post_weight, self.eps, self.scale, T, s.k, s.H, f.y, None, st)
         if update_bias:
             L.moe_bias_update(b.counts, layer.bias, s.E, gamma, st)
+        b.held = Held(keep_gu, seq_len, f, add is not None, shared_w is not None)
         return f.y
 
     def backward(self, dy, x, shared_w=None, stream=None, seq_len: int | None = None,
                  alpha: float = 0.0001):
-        """Backward for the output gradient dy (x's type) after a forward of x
-        (with the same shared_w and seq_len).  Returns (the block's buffers, the
+        """Backward for the output gradient dy (x's type) of the last forward of
+        the layer at this T, which has to be this block's of x (with the same
+        shared_w and seq_len): what a forward leaves for it lies in the layer's
+        buffers, so that batches in flight together, or another type's of the
+        same T, need a layer each.  Returns (the block's buffers, the
         layer's backward buffers): dx - the gradient of x and of add alike -,
         d_weight (with a weight), d_post_weight (with a post_weight) and
         d_shared_w (with shared_w); dC, dW_gu, dW_dn, dw of the layer."""
@@ -896,12 +931,18 @@ class MoEBlock:
             raise ValueError(f"dy {tuple(dy.shape)} {dy.dtype} and x {tuple(x.shape)} {x.dtype} differ")
         self._check_shapes(x, None, shared_w)
         T = dy.shape[0]
-        f = self.buffers(T, dy.dtype)
-        if f.added is None:
-            raise ValueError(f"backward of {T} tokens in {dy.dtype} before a forward of them")
-        if T and not f.added and x.data_ptr() == f.y.data_ptr():
+        f, b = self.buffers(T, dy.dtype), layer.buffers(T)
+        held = b.held
+        if held is None or held.block is not f:
+            raise ValueError(f"backward of {T} tokens in {dy.dtype} before a forward of them, or after another forward "
+                             "on the layer's buffers")
+        if held.gated != (shared_w is not None):
+            raise ValueError(f"backward {'without' if held.gated else 'with'} shared_w of a forward "
+                             f"{'with' if held.gated else 'without'} it")
+        layer._check_seq_len(b, seq_len)
+        if T and not held.added and x.data_ptr() == f.y.data_ptr():
             raise ValueError("x is the block's own y, which the forward has written over: pass a copy of it to both")
-        f, b, bb = f.gradients(), layer.buffers(T), layer.backward_buffers(T)
+        f, bb = f.gradients(), layer.backward_buffers(T)
         st = stream if stream is not None else torch.cuda.current_stream()
         weighted = self.post_weight is not None
         L.moe_combine_norm_backward(
@@ -910,7 +951,7 @@ class MoEBlock:
             f.d_post_weight if weighted else None, f.ws, f.ws_bytes, st)
         layer._experts_backward(f.n, b, bb, False, st, _run)
         layer._router_backward(f.n, b, bb, seq_len, alpha, st, _run)
-        L.moe_norm_backward(bb.dx_total, f.sum if f.added else x, self.weight, f.rstd, dy, self.residual_scale, T,
+        L.moe_norm_backward(bb.dx_total, f.sum if held.added else x, self.weight, f.rstd, dy, self.residual_scale, T,
                             s.H, f.dx, f.d_weight if self.weight is not None else None, f.ws, f.ws_bytes, st)
         return f, bb
 
@@ -923,7 +964,9 @@ class MoEBlock:
             self.forward(x, add, stream=side, **forward_kw)   # warm-up outside the capture
         torch.cuda.current_stream().wait_stream(side)
         torch.cuda.synchronize()
-        graph = torch.cuda.CUDAGraph()
+        graph = CapturedForward()
         with torch.cuda.graph(graph):
             self.forward(x, add, stream=torch.cuda.current_stream(), **forward_kw)
+        graph.bufs = self.layer.buffers(x.shape[0])
+        graph.held = graph.bufs.held
         return graph

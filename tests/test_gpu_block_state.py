@@ -1,0 +1,126 @@
+"""What a forward leaves for the backward, with other forwards between the two:
+called, replayed, of another type, of another block on the same layer."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_block_scaled_bias_amd as M
+import synth
+from bf16_cases import up, values
+from gpu_common import dev, host
+from test_gpu_bf16_layer import bf16_layer
+from test_gpu_gate_int8_layers import build
+from test_gpu_norm import EPS, stream
+
+pytestmark = pytest.mark.gpu
+
+CFG = synth.CONFIGS["mid"]
+LAYERS = {"bf16": lambda: bf16_layer(CFG)[0], "fp8": lambda: build(M.MoELayer, CFG, None)[0]}
+
+
+def weight(seed=1):
+    return dev((1 + 0.1 * np.random.default_rng(seed).standard_normal(CFG.H)).astype(np.float32))
+
+
+def batch(seed, dtype=torch.float32):
+    rng = np.random.default_rng(seed)
+    shape = (CFG.T, CFG.H)
+    return stream(rng, shape, dtype)[1], up(values(rng, shape)), stream(rng, shape, dtype, 0.02)[1]
+
+
+def gradients(block, dy, x, **kw):
+    f, bb = block.backward(dy, x, **kw)
+    return [host(t.float()).copy() for t in (f.dx, f.d_weight, bb.dC, bb.dw, bb.dW_gu, bb.dW_dn)]
+
+
+def same(got, want):
+    for g, w in zip(got, want):
+        assert np.array_equal(g, w)
+
+
+@pytest.mark.parametrize("kind", LAYERS)
+def test_backward_after_another_forward(kind):
+    layer = LAYERS[kind]()
+    block, other = M.MoEBlock(layer, weight(), EPS), M.MoEBlock(layer, weight(2), EPS)
+    x, add, dy = batch(1)
+    x2 = batch(2, torch.bfloat16)[0]
+    with pytest.raises(ValueError, match="before a forward"):
+        block.backward(dy, x)
+    block.forward(x, add, keep_gu=True)
+    want = gradients(block, dy, x)
+    for between in (lambda: block.forward(x2), lambda: other.forward(x), lambda: layer.forward(x2),
+                    lambda: layer.forward(x2, keep_gu=True)):
+        block.forward(x, add, keep_gu=True)
+        between()
+        with pytest.raises(ValueError, match="another forward"):
+            block.backward(dy, x)
+    # (buffers of another number of tokens are others)
+    block.forward(x, add, keep_gu=True)
+    block.forward(x[:-3].contiguous())
+    same(gradients(block, dy, x), want)
+
+
+@pytest.mark.parametrize("kind", LAYERS)
+def test_backward_after_a_replay(kind):
+    """The replayed forward's, whatever was called between capture and replay."""
+    layer = LAYERS[kind]()
+    block, other = M.MoEBlock(layer, weight(), EPS), M.MoEBlock(layer, weight(2), EPS)
+    x, add, dy = batch(1)
+    x2, add2, _ = batch(2)
+    block.forward(x, add, keep_gu=True)
+    want = gradients(block, dy, x)
+    with_add, without = block.capture(x, add, keep_gu=True), block.capture(x2)
+    block.forward(x2, keep_gu=True)
+    want2 = gradients(block, dy, x2)
+    for between in (lambda: block.forward(x2, keep_gu=False), lambda: other.forward(x2), without.replay,
+                    lambda: layer.forward(add2)):
+        between()
+        with_add.replay()
+        same(gradients(block, dy, x), want)
+    for between in (lambda: block.forward(x, add, keep_gu=True), with_add.replay):
+        between()
+        without.replay()   # (gate and up not kept: what lies there is the other's)
+        same(gradients(block, dy, x2), want2)
+
+
+@pytest.mark.parametrize("kind", LAYERS)
+def test_layer_backward_after_a_replay(kind):
+    """keep_gu is the captured forward's, not that of a call in between."""
+    layer = LAYERS[kind]()
+    x, x2, dy = (up(values(np.random.default_rng(i), (CFG.T, CFG.H), s)) for i, s in ((1, 1.0), (2, 1.0), (3, 0.02)))
+
+    def grads():
+        bb = layer.backward(dy, x)
+        return [host(t.float()).copy() for t in (bb.dx_total, bb.dW_gu, bb.dW_dn, bb.dC)]
+    layer.forward(x)
+    want = grads()
+    g = layer.capture(x)
+    layer.forward(x2, keep_gu=True)
+    g.replay()
+    same(grads(), want)
+
+
+def test_backward_as_its_forward():
+    layer = LAYERS["fp8"]()
+    block = M.MoEBlock(layer, weight(), EPS)
+    x, _, dy = batch(1)
+    xb = x.bfloat16()
+    sw = dev(np.random.default_rng(1).random(CFG.T).astype(np.float32))
+    block.forward(x, None, sw)
+    with pytest.raises(ValueError, match="shared_w"):
+        block.backward(dy, x)
+    block.forward(x)
+    with pytest.raises(ValueError, match="shared_w"):
+        block.backward(dy, x, sw)
+    # the balance statistic of an earlier forward is not this one's
+    for f, b in ((lambda **kw: block.forward(x, **kw), lambda **kw: block.backward(dy, x, **kw)),
+                 (lambda **kw: layer.forward(xb, **kw), lambda **kw: layer.backward(xb, xb, **kw))):
+        f(seq_len=16)
+        b(seq_len=16)
+        b()
+        f()
+        with pytest.raises(ValueError, match="seq_len"):
+            b(seq_len=16)
+        f(seq_len=16)
+        with pytest.raises(ValueError, match="seq_len"):
+            b(seq_len=8)
