@@ -860,8 +860,12 @@ class MoEBlock:
     def __init__(self, layer: MoELayer, weight=None, eps: float = 1e-6, post_norm: bool = False,
                  post_weight=None, residual_scale: float = 1.0, scale: float = 1.0):
         for w in (weight, post_weight):
-            if w is not None and w.shape != (layer.shape.H,):
+            if w is None:
+                continue
+            if w.shape != (layer.shape.H,):
                 raise ValueError(f"a norm's weight has the shape [H] = [{layer.shape.H}], not {list(w.shape)}")
+            if L._ptr(w, torch.float32, layer.centroids.get_device()) % 16:
+                raise ValueError("a norm's weight must be 16-byte aligned")
         self.layer, self.weight, self.eps = layer, weight, eps
         self.post_norm, self.post_weight = post_norm, post_weight
         self.residual_scale, self.scale = residual_scale, scale
@@ -873,12 +877,17 @@ class MoEBlock:
             self._bufs[key] = BlockBuffers(self.layer.shape, T, dtype, self.layer.centroids.device)
         return self._bufs[key]
 
-    def _check_shapes(self, x, add, shared_w):
-        H = self.layer.shape.H
+    def _check(self, x, add, shared_w):
+        """All that a call refuses of its tensors, before anything is launched."""
+        H, dev = self.layer.shape.H, L._device()
         if x.dim() != 2 or x.shape[1] != H or (add is not None and add.shape != x.shape):
             raise ValueError(f"x {list(x.shape)}{'' if add is None else f' and add {list(add.shape)}'}: not [T, {H}]")
         if shared_w is not None and shared_w.shape != (x.shape[0],):
             raise ValueError(f"shared_w {list(shared_w.shape)}: not [{x.shape[0]}]")
+        if shared_w is not None and not self.layer.shape.n_shared:
+            raise ValueError("shared_w of a layer without a shared expert")
+        L._logits_type(x, "x")
+        L._ptr(x, None, dev), L._ptr(add, torch.bfloat16, dev), L._ptr(shared_w, torch.float32, dev)
 
     def forward(self, x, add=None, shared_w=None, stream=None, update_bias: bool = False,
                 gamma: float = 0.001, seq_len: int | None = None, alpha: float = 0.0001,
@@ -889,17 +898,17 @@ class MoEBlock:
         this T and type (buffers(T, x.dtype).sum holds v after an add)."""
         layer, s = self.layer, self.layer.shape
         layer._check_gate(seq_len)
-        self._check_shapes(x, add, shared_w)
+        self._check(x, add, shared_w)
         if keep_gu and isinstance(layer, Int8MoELayer):
             raise ValueError("keep_gu is for the backward, which an Int8MoELayer does not have")
         T = x.shape[0]
         f, b = self.buffers(T, x.dtype), layer.buffers(T)
         st = stream if stream is not None else torch.cuda.current_stream()
-        b.held = None
         v = f.sum if add is not None else x
         codes, scales = (None, None) if layer.CODES == L.QUANT_NONE else (b.xq, b.xs)
         L.moe_norm(x, add, self.weight, T, s.H, self.eps, None if add is None else v, f.n, f.rstd, layer.CODES,
                    codes, scales, st)
+        b.held = None
         layer._route(f.n, b, seq_len, st)
         if seq_len is not None:
             layer._seq_balance(b, seq_len, alpha, st)
@@ -929,7 +938,10 @@ class MoEBlock:
         layer._check_backward(seq_len)
         if dy.dtype != x.dtype or dy.shape != x.shape:
             raise ValueError(f"dy {tuple(dy.shape)} {dy.dtype} and x {tuple(x.shape)} {x.dtype} differ")
-        self._check_shapes(x, None, shared_w)
+        self._check(x, None, shared_w)
+        L._ptr(dy, None, L._device())
+        if dy.data_ptr() % 16 or x.data_ptr() % 16:
+            raise ValueError("dy and x must be 16-byte aligned")
         T = dy.shape[0]
         f, b = self.buffers(T, dy.dtype), layer.buffers(T)
         held = b.held

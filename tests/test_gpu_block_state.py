@@ -124,3 +124,41 @@ def test_backward_as_its_forward():
         f(seq_len=16)
         with pytest.raises(ValueError, match="seq_len"):
             b(seq_len=8)
+
+
+def test_refused_before_anything_is_launched():
+    """A refused call leaves what the last forward left."""
+    for shared in (1, 0):
+        cfg = CFG.with_(n_shared=shared)
+        layer = bf16_layer(cfg)[0]
+        block = M.MoEBlock(layer, weight(), EPS)
+        x, add, dy = batch(1)
+        x2 = batch(2)[0]
+        T, H = cfg.T, cfg.H
+        sw = torch.rand(T, device="cuda")
+        block.forward(x, add, keep_gu=True)
+        want = gradients(block, dy, x)
+        f, b = block.buffers(T, x.dtype), layer.buffers(T)
+        kept = [t.clone() for t in (f.n, f.sum, f.rstd, f.y, b.d, b.h, b.hgu, b.topk_w, b.inv_perm)]
+        wide = torch.zeros((T, 2 * H), device="cuda")
+        loose = torch.zeros(T * H + 1, device="cuda")[1:].view(T, H)   # not 16-byte aligned
+        bad = [lambda: block.forward(x2, None, sw.double()), lambda: block.forward(x2, None, sw.cpu()),
+               lambda: block.forward(x2, None, torch.rand(2 * T, device="cuda")[::2]),
+               lambda: block.forward(x2, add.float()), lambda: block.forward(x2, add.t().contiguous().t()),
+               lambda: block.forward(x2.half()), lambda: block.forward(wide[:, ::2]), lambda: block.forward(loose),
+               lambda: block.backward(dy, loose), lambda: block.backward(loose, x), lambda: block.backward(dy, wide[:, ::2]),
+               lambda: block.backward(wide[:, ::2], x)]
+        if not shared:
+            bad += [lambda: block.forward(x2, None, sw), lambda: block.backward(dy, x, sw)]
+        for i, call in enumerate(bad):
+            with pytest.raises((ValueError, TypeError, M.MoEError)):
+                call()
+            torch.cuda.synchronize()
+            for t, k in zip((f.n, f.sum, f.rstd, f.y, b.d, b.h, b.hgu, b.topk_w, b.inv_perm), kept):
+                assert torch.equal(t.view(torch.uint8), k.view(torch.uint8)), i
+        same(gradients(block, dy, x), want)
+        H2 = torch.ones(2 * H, device="cuda")
+        for w in (H2[:H].double(), H2[:H].cpu(), H2[::2], H2[1:H + 1]):
+            for kw in (dict(weight=w), dict(post_norm=True, post_weight=w)):
+                with pytest.raises((ValueError, TypeError)):
+                    M.MoEBlock(layer, **kw)
