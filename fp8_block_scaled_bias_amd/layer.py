@@ -371,6 +371,7 @@ class MoELayer:
         s = self.shape
         T = x_bf16.shape[0]
         b = bufs or self.buffers(T)
+        self._check_rows(b, x_bf16)
         st = stream if stream is not None else torch.cuda.current_stream()
         if self._side is None:
             self._side = torch.cuda.Stream(device=st.device)
@@ -486,8 +487,11 @@ class MoELayer:
         s = self.shape
         T = dy_bf16.shape[0]
         b = bufs or self.buffers(T)
+        self._check_rows(b, dy_bf16, x_bf16)
         self._check_seq_len(b, seq_len)
         bb = bwd or self.backward_buffers(T)
+        if bb.T != T:
+            raise ValueError(f"backward buffers of {bb.T} tokens for {T}")
         if keep_intermediates:
             bb.intermediates()
         st = stream if stream is not None else torch.cuda.current_stream()
@@ -582,6 +586,16 @@ class MoELayer:
         if self.gate is not None and self.shape.E % 16:
             raise ValueError(f"the backward of a layer with a Gate needs E % 16 == 0, E is {self.shape.E}")
 
+    def _check_rows(self, b, *tensors):
+        """The layer's inputs, before anything is launched: the kernels take
+        their sizes from the shape."""
+        for t in tensors:
+            if t.dim() != 2 or t.shape != (b.T, self.shape.H):
+                raise ValueError(f"{list(t.shape)} in buffers of [T, H] = [{b.T}, {self.shape.H}]")
+        dev = L._device()
+        for t in tensors:
+            L._ptr(t, torch.bfloat16, dev)
+
     @staticmethod
     def _check_seq_len(b, seq_len):
         if seq_len is not None and (b.held is None or b.held.seq_len != seq_len):
@@ -668,6 +682,7 @@ class Int8MoELayer(MoELayer):
         s = self.shape
         T = x_bf16.shape[0]
         b = bufs or self.buffers(T)
+        self._check_rows(b, x_bf16)
         st = stream if stream is not None else torch.cuda.current_stream()
         if self._side is None:
             self._side = torch.cuda.Stream(device=st.device)
