@@ -20,6 +20,8 @@ typedef int v2i __attribute__((ext_vector_type(2)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 constexpr int MAXG = 1024;  // groups the LDS tile tables hold
+// Rows of a call: the kernels count up to the end of a tile of 256 rows in 32 bits.
+constexpr int64_t kMaxRows = (1ll << 31) - 256;
 
 struct GemmArgs {
   const uint8_t* A;

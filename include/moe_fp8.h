@@ -29,6 +29,7 @@
  *     outputs must not alias (except where a call says "in place").
  *   - A zero-sized problem (T == 0, M_total == 0) is a successful no-op that
  *     still writes the outputs that do not depend on it (counts, offsets).
+ *   - Calls with group_offsets take at most M_total = 2^31 - 256 rows.
  *   - NaN or Inf inputs give unspecified results.
  */
 #ifndef MOE_FP8_H
