@@ -80,10 +80,28 @@ bf16 weights; every step runs in the library's HIP kernels.
 from __future__ import annotations
 
 import dataclasses
+import functools
+import inspect
 
 import torch
 
 from . import _lib as L
+
+
+def _on_stream(call):
+    """call with its `stream`, if one is given, as the current one: what it
+    allocates and fills the first time comes before its launches there, and not
+    in the order of whatever other stream was current."""
+    where = list(inspect.signature(call).parameters).index("stream")
+
+    @functools.wraps(call)
+    def on_stream(*args, **kw):
+        st = args[where] if len(args) > where else kw.get("stream")
+        if not isinstance(st, torch.cuda.Stream) or st == torch.cuda.current_stream():
+            return call(*args, **kw)
+        with torch.cuda.stream(st):
+            return call(*args, **kw)
+    return on_stream
 
 
 @dataclasses.dataclass(frozen=True)
@@ -344,6 +362,7 @@ class MoELayer:
             b = self._bufs[T] = Buffers(self.shape, T, self.centroids.device)
         return b
 
+    @_on_stream
     def forward(self, x_bf16: torch.Tensor, bufs: Buffers | None = None, stream=None,
                 update_bias: bool = False, gamma: float = 0.001,
                 events: dict | None = None,
@@ -465,6 +484,7 @@ class MoELayer:
             bb = self._bwd[T] = BackwardBuffers(self.shape, T, self.centroids.device)
         return bb
 
+    @_on_stream
     def backward(self, dy_bf16: torch.Tensor, x_bf16: torch.Tensor, bufs: Buffers | None = None,
                  bwd: BackwardBuffers | None = None, stream=None, events: dict | None = None,
                  seq_len: int | None = None, alpha: float = 0.0001,
@@ -675,6 +695,7 @@ class Int8MoELayer(MoELayer):
             b = self._bufs[T] = Int8Buffers(self.shape, T, self.centroids.device)
         return b
 
+    @_on_stream
     def forward(self, x_bf16: torch.Tensor, bufs: Int8Buffers | None = None, stream=None,
                 update_bias: bool = False, gamma: float = 0.001) -> torch.Tensor:
         """One layer forward (x's quantisation beside the router, as in
@@ -904,6 +925,7 @@ class MoEBlock:
         L._logits_type(x, "x")
         L._ptr(x, None, dev), L._ptr(add, torch.bfloat16, dev), L._ptr(shared_w, torch.float32, dev)
 
+    @_on_stream
     def forward(self, x, add=None, shared_w=None, stream=None, update_bias: bool = False,
                 gamma: float = 0.001, seq_len: int | None = None, alpha: float = 0.0001,
                 keep_gu: bool = False) -> torch.Tensor:
@@ -937,6 +959,7 @@ class MoEBlock:
         b.held = Held(keep_gu, seq_len, f, add is not None, shared_w is not None)
         return f.y
 
+    @_on_stream
     def backward(self, dy, x, shared_w=None, stream=None, seq_len: int | None = None,
                  alpha: float = 0.0001):
         """Backward for the output gradient dy (x's type) of the last forward of
