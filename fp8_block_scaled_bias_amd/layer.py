@@ -757,7 +757,7 @@ class Bf16BackwardBuffers(BackwardBuffers):
 
     def _operands(self):
         self.dgu = torch.empty((self.R, 2 * self._shape.I), dtype=torch.bfloat16, device=self._dev)
-        self.dDq = self.dDs = self._gu = None
+        self.dDq = self.dDs = self._gu = self.h = None
 
     @property
     def gu(self):
@@ -829,6 +829,8 @@ class Bf16MoELayer(MoELayer):
     def _experts_backward(self, x_bf16, b, bb, keep_intermediates, st, step):
         s = self.shape
         R, G, H, I = b.R, s.G, s.H, s.I
+        if keep_intermediates:   # (dGU and h are the products' own operands)
+            bb.h = b.h
         if b.held is not None and b.held.gu:
             gu = b.hgu
         else:

@@ -162,3 +162,20 @@ def test_refused_before_anything_is_launched():
             for kw in (dict(weight=w), dict(post_norm=True, post_weight=w)):
                 with pytest.raises((ValueError, TypeError)):
                     M.MoEBlock(layer, **kw)
+
+
+def test_intermediates_of_a_bf16_layer():
+    """keep_intermediates: dGU and h, whose products are the weights' gradients."""
+    layer = LAYERS["bf16"]()
+    x, dy = (up(values(np.random.default_rng(i), (CFG.T, CFG.H), s)) for i, s in ((1, 1.0), (2, 0.02)))
+    layer.forward(x)
+    bb = layer.backward(dy, x, keep_intermediates=True)
+    b = layer.buffers(CFG.T)
+    offs = host(b.offsets)
+    g = int(np.argmax(np.diff(offs)))
+    r = slice(int(offs[g]), int(offs[g + 1]))
+    h, dD, dgu = (t[r].double() for t in (bb.h, bb.dD, bb.dgu))
+    xs = x[b.perm_src[r].long()].double()
+    # (fp32 sums over the group's rows: at most so many roundings of 2^-24 in the norm)
+    for got, want in ((bb.dW_dn[g], dD.t() @ h), (bb.dW_gu[g], dgu.t() @ xs)):
+        assert torch.linalg.norm(got.double() - want) <= len(h) * 2.0 ** -24 * torch.linalg.norm(want)
