@@ -154,6 +154,8 @@ class CapturedForward(torch.cuda.CUDAGraph):
     def replay(self):
         super().replay()
         self.bufs.held = self.held
+        if self.held.seq_len is not None:
+            self.bufs.balance(self.held.seq_len)
 
 
 class Buffers:
@@ -180,6 +182,7 @@ class Buffers:
         self.perm_ws = torch.empty((self.perm_ws_bytes,), dtype=u8, device=dev)
         self._hgu = None
         self._logits = None
+        self._balance = {}
         self._dev = dev
         self._shape = s
         self.d = torch.empty((R, s.H), dtype=bf, device=dev)
@@ -196,21 +199,24 @@ class Buffers:
         self.hs = torch.empty((R, s.I // 128), dtype=f32, device=dev)
 
     def balance(self, seq_len: int):
-        """Buffers of the sequence-wise balance statistic (allocated on first
-        use, again when seq_len changes): scores [T, E], score_sums [T],
-        seq_f, seq_p [B, E], seq_loss [B], B = ceil(T / seq_len)."""
-        s = self._shape
-        if getattr(self, "_seq_len", None) != seq_len:
-            T, dev, f32 = self.T, self._dev, torch.float32
+        """Buffers of the sequence-wise balance statistic (allocated on first use
+        and kept for each seq_len, which a captured graph may write): scores
+        [T, E], score_sums [T], seq_f, seq_p [B, E], seq_loss [B], B = ceil(T /
+        seq_len).  The names hold the last seq_len's."""
+        s, T = self._shape, self.T
+        if seq_len not in self._balance:
+            dev, f32 = self._dev, torch.float32
             B = -(-T // seq_len)
-            self.scores = torch.empty((max(T, 1), s.E), dtype=f32, device=dev)
-            self.score_sums = torch.empty((max(T, 1),), dtype=f32, device=dev)
-            self.seq_f = torch.empty((max(B, 1), s.E), dtype=f32, device=dev)
-            self.seq_p = torch.empty((max(B, 1), s.E), dtype=f32, device=dev)
-            self.seq_loss = torch.empty((max(B, 1),), dtype=f32, device=dev)
-            self.seq_ws_bytes = max(16, L.moe_seq_balance_workspace_bytes(T, s.E, seq_len))
-            self.seq_ws = torch.empty((self.seq_ws_bytes,), dtype=torch.uint8, device=dev)
-            self._seq_len = seq_len
+            ws_bytes = max(16, L.moe_seq_balance_workspace_bytes(T, s.E, seq_len))
+            self._balance[seq_len] = dict(
+                scores=torch.empty((max(T, 1), s.E), dtype=f32, device=dev),
+                score_sums=torch.empty((max(T, 1),), dtype=f32, device=dev),
+                seq_f=torch.empty((max(B, 1), s.E), dtype=f32, device=dev),
+                seq_p=torch.empty((max(B, 1), s.E), dtype=f32, device=dev),
+                seq_loss=torch.empty((max(B, 1),), dtype=f32, device=dev),
+                seq_ws_bytes=ws_bytes,
+                seq_ws=torch.empty((ws_bytes,), dtype=torch.uint8, device=dev))
+        vars(self).update(self._balance[seq_len])
         return self
 
     @property
@@ -595,6 +601,7 @@ class MoELayer:
                 L.moe_router_dcentroids(x_bf16, b.perm_src, b.offsets, bb.dlogit_rows, T, H, s.E,
                                         bb.dC, st)))
         else:
+            b.balance(seq_len)   # (the names may hold another's)
             bb.dense()
             step("router_bwd", lambda: L.moe_router_backward_dense(
                 x_bf16, self.centroids, b.topk_idx, bb.dw, b.scores, b.score_sums, b.seq_f, T, H,

@@ -179,3 +179,30 @@ def test_intermediates_of_a_bf16_layer():
     # (fp32 sums over the group's rows: at most so many roundings of 2^-24 in the norm)
     for got, want in ((bb.dW_dn[g], dD.t() @ h), (bb.dW_gu[g], dgu.t() @ xs)):
         assert torch.linalg.norm(got.double() - want) <= len(h) * 2.0 ** -24 * torch.linalg.norm(want)
+
+
+@pytest.mark.parametrize("what", ["layer", "block"])
+def test_replay_with_a_balance_term(what):
+    """The statistic of a captured seq_len after a forward of another one."""
+    layer = LAYERS["fp8"]()
+    b = layer.buffers(CFG.T)
+    if what == "block":
+        call, (x, _, dy) = M.MoEBlock(layer, weight(), EPS), batch(1)
+        dx = lambda bb: bb[0].dx
+        bwd = lambda bb: bb[1]
+    else:
+        call = layer
+        x, dy = (up(values(np.random.default_rng(i), (CFG.T, CFG.H), s)) for i, s in ((1, 1.0), (2, 0.02)))
+        dx, bwd = lambda bb: bb.dx_total, lambda bb: bb
+
+    def results():
+        bb = call.backward(dy, x, seq_len=16, alpha=2.0)
+        return [host(t.float()).copy() for t in (dx(bb), bwd(bb).dC, b.seq_loss, b.seq_f, b.scores)]
+    call.forward(x, seq_len=16, alpha=2.0)
+    want = results()
+    g = call.capture(x, seq_len=16, alpha=2.0)
+    call.forward(x, seq_len=64, alpha=2.0)
+    room = [torch.full((n,), 7.0, device="cuda") for n in (b.scores.numel(), CFG.T, 64, 1024, 4096) for _ in range(8)]
+    g.replay()
+    same(results(), want)
+    assert all((t == 7).all() for t in room)
