@@ -303,6 +303,15 @@ class BackwardBuffers:
         self.s_x = torch.empty((c, H), dtype=f32, device=dev)
 
 
+def _check_weights(w, out):
+    """New weights are fp32 of the shape that they replace: the kernels take
+    their sizes from it, and a copy would repeat one expert's for all."""
+    if w.dtype != torch.float32:
+        raise TypeError(f"weights must be float32, not {w.dtype}")
+    if w.shape != out.shape:
+        raise ValueError(f"weights {list(w.shape)} in the place of {list(out.shape)}")
+
+
 def _run(name, *args):
     """A step that is not timed."""
     args[-1]()
@@ -341,6 +350,7 @@ class MoELayer:
     @staticmethod
     def quantize_into(w_f32, out_q, out_s, stream=None):
         """128x128 block quantisation of fp32 weights [G', N, K] into E4M3 + scales."""
+        _check_weights(w_f32, out_q)
         G, N, K = w_f32.shape
         L.fp8_quant_128x128(w_f32, G, N, K, out_q, out_s, stream)
 
@@ -457,11 +467,11 @@ class MoELayer:
 
     def requantize_from_fp32(self, gu_fp32, dn_fp32, stream=None):
         """Requantise both weight sets in place from fp32 master weights
-        ([G, 2I, H] and [G, H, I] device tensors) in 128x128 blocks (the
+        ([G, 2I, H] and [G, H, I] device tensors), as quantize_into does (the
         per-update cast after an optimizer step)."""
-        s = self.shape
-        L.fp8_quant_128x128(gu_fp32, s.G, 2 * s.I, s.H, self.w_gu, self.w_gu_s, stream)
-        L.fp8_quant_128x128(dn_fp32, s.G, s.H, s.I, self.w_dn, self.w_dn_s, stream)
+        _check_weights(dn_fp32, self.w_dn)   # (before the other is written)
+        self.quantize_into(gu_fp32, self.w_gu, self.w_gu_s, stream)
+        self.quantize_into(dn_fp32, self.w_dn, self.w_dn_s, stream)
 
     def capture(self, x_bf16: torch.Tensor, bufs: Buffers | None = None, **forward_kw):
         """One forward captured as a HIP graph (torch.cuda.CUDAGraph); its
@@ -693,6 +703,7 @@ class Int8MoELayer(MoELayer):
     @staticmethod
     def quantize_into(w_f32, out_q, out_s, stream=None):
         """Quantisation of fp32 weights [G', N, K], one scale an output channel."""
+        _check_weights(w_f32, out_q)
         G, N, K = w_f32.shape
         L.int8_quant_channels(w_f32, G, N, K, out_q, out_s, stream)
 
@@ -740,12 +751,6 @@ class Int8MoELayer(MoELayer):
         L.int8_quant_rows(b.h, R, s.I, s.I, b.hq, b.hs, st)
         L.grouped_int8_gemm(b.hq, b.hs, None, self.w_dn, self.w_dn_s, b.offsets, s.G, R, s.H, s.I,
                             b.d, st)
-
-    def requantize_from_fp32(self, gu_fp32, dn_fp32, stream=None):
-        """Requantise both weight sets in place from fp32 weights ([G, 2I, H]
-        and [G, H, I] device tensors)."""
-        self.quantize_into(gu_fp32, self.w_gu, self.w_gu_s, stream)
-        self.quantize_into(dn_fp32, self.w_dn, self.w_dn_s, stream)
 
     def backward(self, *args, **kw):
         raise NotImplementedError("Int8MoELayer is a forward only: train with MoELayer")
@@ -800,6 +805,7 @@ class Bf16MoELayer(MoELayer):
     @staticmethod
     def quantize_into(w_f32, out_q, out_s=None, stream=None):
         """fp32 weights rounded to bf16."""
+        _check_weights(w_f32, out_q)
         st = stream if stream is not None else torch.cuda.current_stream()
         with torch.cuda.stream(st):
             out_q.copy_(w_f32)
@@ -815,12 +821,6 @@ class Bf16MoELayer(MoELayer):
         if bb is None:
             bb = self._bwd[T] = Bf16BackwardBuffers(self.shape, T, self.centroids.device)
         return bb
-
-    def requantize_from_fp32(self, gu_fp32, dn_fp32, stream=None):
-        """Both weight sets in place from fp32 master weights ([G, 2I, H] and
-        [G, H, I] device tensors), rounded to bf16."""
-        self.quantize_into(gu_fp32, self.w_gu, None, stream)
-        self.quantize_into(dn_fp32, self.w_dn, None, stream)
 
     def _quantise(self, x_bf16, b, stream):
         pass

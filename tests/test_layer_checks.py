@@ -56,3 +56,15 @@ def test_other_types_and_places(layer, monkeypatch):
             layer.backward(rows(T, S.H).float(), rows(T, S.H))
         with pytest.raises(ValueError, match="tokens"):
             layer.backward(rows(T, S.H), rows(T, S.H), bwd=layer.backward_buffers(T + 1))
+
+
+def test_new_weights(layer):
+    gu, dn = torch.zeros(S.G, 2 * S.I, S.H), torch.zeros(S.G, S.H, S.I)
+    before = layer.w_gu.clone()
+    for a, b in ((gu[:1], dn), (gu, dn[:1]), (gu[:, :1], dn), (gu, dn.transpose(1, 2).contiguous()), (gu[0], dn)):
+        with pytest.raises(ValueError, match="weights"):
+            layer.requantize_from_fp32(a, b)
+    for a, b in ((gu.double(), dn), (gu, dn.bfloat16())):
+        with pytest.raises(TypeError, match="float32"):
+            layer.requantize_from_fp32(a, b)
+    assert torch.equal(layer.w_gu.view(torch.uint8), before.view(torch.uint8))
