@@ -186,6 +186,7 @@ __global__ __launch_bounds__(ST) void split_kernel(typename E::Args a) {
 template <class E, int MB, int D, bool GLU>
 __global__ __launch_bounds__(ST) void flow_kernel(typename E::Args a) {
   constexpr int NJ = 4, NO = GLU ? 2 : 4;
+  static_assert(!E::kClearB, "what is past a row's end is cleared in one operand only");
   __shared__ int s_offs[MAXG + 1];
   __shared__ int s_pref[MAXG + 1];
   __shared__ int s_red[4];
@@ -316,9 +317,6 @@ __global__ __launch_bounds__(ST) void flow_kernel(typename E::Args a) {
             if (c_k * 128 + 64 * h + 16 * q >= (int)K) {
 #pragma unroll
               for (int i = 0; i < MB; ++i) xa[i][h] = v4i{0, 0, 0, 0};
-              if (E::kClearB)
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) xb[j][h] = v4i{0, 0, 0, 0};
             }
         }
 #pragma unroll
