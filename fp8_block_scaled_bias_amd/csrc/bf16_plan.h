@@ -42,16 +42,31 @@ inline int64_t n16(const Shape& s) { return parts(s.N, s.mode == kGlu ? 8 : 16);
 
 // A 256 x 256 tile takes as long as two of 128 x 128, one a CU, so the wide
 // tiles are taken where they save more than half of the rounds of the CUs.
-// Times (wide / mid), 64 groups, N = 4096, K = 7168: 17 rows 690 / 625 us, 64:
-// 733 / 682, 128: 792 / 778, 256: 908 / 1259; one group: 1024 rows 132 / 71, 2048:
-// 141 / 137, 4096: 187 / 281; the input gradient of one group: 1024 rows 93 / 87,
-// 2048: 107 / 167.
+// Times in us, 256 x 256 / 128 x 128 tiles, N x K of the weights:
+//                          4096 x 7168      7168 x 2048
+//   64 groups,  17 rows    690 / 656        354 / 346
+//               64         725 / 714        387 / 396
+//              128         770 / 799        409 / 437
+//              192         840 / 1446       453 / 691
+//              256         893 / 1283       483 / 705
+//   one group, 1024 rows   119 / 74          42 / 43
+//             1536         117 / 121         46 / 63
+//             2048         129 / 138         53 / 85
+//             4096         171 / 281        100 / 163
+//   input gradient of one group
+//             1024          83 / 84         135 / 72
+//             2048         101 / 164        138 / 84
+//             4096         203 / 317        152 / 153
+// The rule takes the faster one but where they are within 8 %.
 //
 // The register kernels where there are too few tiles for the CUs: of few rows
-// (16 rows of one group 15 us, 55 with 128 x 128 tiles; four groups 35 and 58,
-// eight 82 and 83) and of up to a 64 x 64 tile a CU (256 rows of one group 54
-// and 57 us).  The widest column tile that gives every CU one: 64 rows of one
-// group 53 us with 64, 40 with 32, 35 with 16 weight rows.
+// (16 rows of one group 15 us, 56 with 128 x 128 tiles, 4096 x 7168; 9.3 and 20,
+// 7168 x 2048) and of up to a 64 x 64 tile a CU (256 rows of one group 54 and 58
+// us, 4096 x 7168).  The widest column tile that gives every CU one: 64 rows of one
+// group 52 us with 64, 40 with 32, 34 with 16 weight rows (7168 x 2048, where 224
+// tiles of 32 are not one a CU: 18, 14 and 21 us).  Their row tiles are
+// counted as the most that there can be, so that four groups of 16 rows each are
+// left to the tiles (57 us; 34 in registers), as eight are (85 and 83).
 inline Plan plan(const Shape& s, int64_t cus) {
   const int64_t avg = s.M_total / s.G;
   const int64_t rows = s.mode == kWgrad ? s.N : avg;

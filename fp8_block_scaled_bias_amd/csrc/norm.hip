@@ -5,15 +5,16 @@
 //
 // HBM bound: a workgroup holds a whole row (or a token's k + 1 rows) in
 // registers, 8 columns a thread and chunk, between the row's sums and what
-// they scale, so that nothing is read twice.  Sums are formed in fp32, over a
-// thread's columns, the wave (DPP) and the waves (LDS) in a fixed order.  The
-// backward passes run a fixed number of workgroups over the tokens, each with
-// its part of the weight's gradient in registers; the parts are added up, in
-// order, by a second launch.
+// they scale, so that nothing is read twice (but by the combine's gradient of
+// more than 8192 columns, whose rows do not fit: they are read twice).  Sums are
+// formed in fp32, over a thread's columns, the wave (DPP) and the waves (LDS) in a
+// fixed order.  The backward passes run a fixed number of workgroups over the
+// tokens, each with its part of the weight's gradient in registers; a second
+// launch adds up the parts, in a fixed order.
 //
 // 16384 x 7168 (HBM reads 6.05, copies 4.7 TB/s): norm of fp32 with the add and
-// E4M3 codes 265 us (5.8 TB/s), its gradient in bf16 184 us (5.1); combine of 8
-// rows and the shared one with norm 474 us (5.4), its gradient with codes 1290
+// E4M3 codes 266 us (5.8 TB/s), its gradient in bf16 183 us (5.1); combine of 8
+// rows and the shared one with norm 475 us (5.4), its gradient with codes 1290
 // us (4.3).  128 rows: 4.9 us, a launch and one row's chain of steps; the weight
 // loaded ahead of the sums gains nothing there and costs 4 % at 16384.
 #include "gemm_common.h"
@@ -294,8 +295,8 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBwdArgs a) {
   }
 }
 
-// out[h] = sum over the parts, in order: RG groups of threads take every RG-th
-// part of 64 columns, their sums meet in LDS.  (P = 0: zero.)
+// out[h] = sum over the parts, in a fixed order: RG groups of threads take every
+// RG-th part of 64 columns, their sums meet in LDS.  (P = 0: zero.)
 constexpr int RG = 64, RD = 16 * RG;
 __global__ __launch_bounds__(RD) void add_parts_kernel(const float* part, int P, int64_t H, float* out) {
   __shared__ float4 s[RG][16];

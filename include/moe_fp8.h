@@ -821,7 +821,8 @@ int grouped_bf16_wgrad(const void* dY_bf16, const void* A_bf16, const int32_t* a
  *   MOE_QUANT_E4M3  codes [T, H] e4m3, scales [T, H/128]: fp8_quant_1x128's rule
  *   MOE_QUANT_INT8  codes [T, H] int8, scales [T]: int8_quant_rows' rule, the
  *                   quotient rounded to fp32 before it is to a whole number
- * in fp32: a row's squares have to stay under the largest fp32 number.
+ * in fp32: a row's squares have to stay under the largest fp32 number, and with
+ * an eps under 2^-126 their mean above that (a row of zeros gives NaN with eps 0).
  * x        [T, H] fp32 or bf16 (x_type MOE_TYPE_*)
  * add_bf16 [T, H] bf16 or NULL;  sum_out (out) [T, H] of x_type, given if and
  *          only if add is; may equal x
