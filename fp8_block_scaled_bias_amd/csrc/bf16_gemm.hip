@@ -17,7 +17,8 @@ int run(const char* who, Mode m, const Args& a, const char* n_name, const char* 
   MOE_UNSUPPORTED(a.G <= gemm::MAXG, "%s: G=%d > %d groups is not supported", who, a.G, gemm::MAXG);
   MOE_INVALID(a.M_total >= 0 && a.M_total < (1ll << 31), "%s: M_total=%lld out of range", who,
               (long long)a.M_total);
-  MOE_UNSUPPORTED(a.M_total <= gemm::kMaxRows, "%s: M_total=%lld > 2^31 - 256 is not supported", who, (long long)a.M_total);
+  MOE_UNSUPPORTED(a.M_total <= gemm::kMaxRows, "%s: M_total=%lld > 2^31 - 256 is not supported", who,
+                  (long long)a.M_total);
   MOE_INVALID(a.N > 0 && a.N % 8 == 0, "%s: %s=%lld must be a positive multiple of 8", who, n_name,
               (long long)a.N);
   MOE_INVALID(a.K > 0 && a.K % 8 == 0, "%s: %s=%lld must be a positive multiple of 8", who, k_name,

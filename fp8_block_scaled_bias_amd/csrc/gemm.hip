@@ -602,7 +602,8 @@ int validate_common(const char* who, const uint8_t* A, const float* A_scale,
   MOE_UNSUPPORTED(G <= MAXG, "%s: G=%d > %d groups is not supported", who, (int)G, MAXG);
   MOE_INVALID(M_total >= 0 && M_total < (1ll << 31), "%s: M_total=%lld out of range", who,
               (long long)M_total);
-  MOE_UNSUPPORTED(M_total <= gemm::kMaxRows, "%s: M_total=%lld > 2^31 - 256 is not supported", who, (long long)M_total);
+  MOE_UNSUPPORTED(M_total <= gemm::kMaxRows, "%s: M_total=%lld > 2^31 - 256 is not supported", who,
+                  (long long)M_total);
   MOE_INVALID(N > 0 && N % 128 == 0, "%s: N=%lld must be a positive multiple of 128", who,
               (long long)N);
   MOE_INVALID(K > 0 && K % 128 == 0, "%s: K=%lld must be a positive multiple of 128", who,

@@ -20,7 +20,8 @@ int int8_gemm(const char* who, bool swiglu, const int8_t* A, const float* A_scal
   MOE_UNSUPPORTED(G <= 1024, "%s: G=%d > 1024 groups is not supported", who, (int)G);
   MOE_INVALID(M_total >= 0 && M_total < (1ll << 31), "%s: M_total=%lld out of range", who,
               (long long)M_total);
-  MOE_UNSUPPORTED(M_total <= gemm::kMaxRows, "%s: M_total=%lld > 2^31 - 256 is not supported", who, (long long)M_total);
+  MOE_UNSUPPORTED(M_total <= gemm::kMaxRows, "%s: M_total=%lld > 2^31 - 256 is not supported", who,
+                  (long long)M_total);
   MOE_INVALID(N > 0 && N % 8 == 0, "%s: %s=%lld must be a positive multiple of 8", who,
               swiglu ? "I" : "N", (long long)N);
   MOE_INVALID(K > 0 && K % 16 == 0, "%s: K=%lld must be a positive multiple of 16", who, (long long)K);

@@ -518,7 +518,8 @@ extern "C" int fp8_quant_128x1_grouped(const void* in_bf16, int64_t ld_in,
   MOE_UNSUPPORTED(G <= gemm::MAXG, "fp8_quant_128x1_grouped: G=%d > %d", (int)G, gemm::MAXG);
   MOE_INVALID(M_total >= 0 && M_total < (1ll << 31), "fp8_quant_128x1_grouped: M_total=%lld out of range",
               (long long)M_total);
-  MOE_UNSUPPORTED(M_total <= gemm::kMaxRows, "fp8_quant_128x1_grouped: M_total=%lld > 2^31 - 256 is not supported", (long long)M_total);
+  MOE_UNSUPPORTED(M_total <= gemm::kMaxRows, "fp8_quant_128x1_grouped: M_total=%lld > 2^31 - 256 is not supported",
+                  (long long)M_total);
   MOE_INVALID(C > 0 && C % 128 == 0 && C / 128 <= 65535,
               "fp8_quant_128x1_grouped: C=%lld must be a positive multiple of 128 (at most 65535*128)",
               (long long)C);
@@ -555,7 +556,8 @@ extern "C" int swiglu_backward_grouped(const void* gu_bf16, const void* dh_bf16,
   MOE_UNSUPPORTED(G <= gemm::MAXG, "swiglu_backward_grouped: G=%d > %d", (int)G, gemm::MAXG);
   MOE_INVALID(M_total >= 0 && M_total < (1ll << 31),
               "swiglu_backward_grouped: M_total=%lld out of range", (long long)M_total);
-  MOE_UNSUPPORTED(M_total <= gemm::kMaxRows, "swiglu_backward_grouped: M_total=%lld > 2^31 - 256 is not supported", (long long)M_total);
+  MOE_UNSUPPORTED(M_total <= gemm::kMaxRows, "swiglu_backward_grouped: M_total=%lld > 2^31 - 256 is not supported",
+                  (long long)M_total);
   MOE_INVALID(I > 0 && I % 128 == 0 && I / 128 <= 65535,
               "swiglu_backward_grouped: I=%lld must be a positive multiple of 128", (long long)I);
   if (M_total == 0) return MOE_OK;
@@ -589,7 +591,8 @@ extern "C" int grouped_fp8_wgrad(const uint8_t* dy_c, const float* dy_scale_c, c
   MOE_INVALID(G >= 1 && G <= 65535, "grouped_fp8_wgrad: G=%d out of [1, 65535]", (int)G);
   MOE_INVALID(M_total >= 0 && M_total < (1ll << 31), "grouped_fp8_wgrad: M_total=%lld out of range",
               (long long)M_total);
-  MOE_UNSUPPORTED(M_total <= gemm::kMaxRows, "grouped_fp8_wgrad: M_total=%lld > 2^31 - 256 is not supported", (long long)M_total);
+  MOE_UNSUPPORTED(M_total <= gemm::kMaxRows, "grouped_fp8_wgrad: M_total=%lld > 2^31 - 256 is not supported",
+                  (long long)M_total);
   MOE_INVALID(N > 0 && N % 128 == 0 && K > 0 && K % 128 == 0,
               "grouped_fp8_wgrad: N=%lld and K=%lld must be positive multiples of 128", (long long)N,
               (long long)K);

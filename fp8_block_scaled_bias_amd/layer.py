@@ -1002,6 +1002,9 @@ class MoEBlock:
         if T and not held.added and x.data_ptr() == f.y.data_ptr():
             raise ValueError("x is the block's own y, which the forward has written over: pass a copy of it to both")
         f, bb = f.gradients(), layer.backward_buffers(T)
+        written = (bb.dx.data_ptr(), bb.dx_total.data_ptr(), bb.dD.data_ptr(), bb.dxp.data_ptr())
+        if T and (dy.data_ptr() in written or x.data_ptr() in written):
+            raise ValueError("dy and x are read after the layer's backward buffers are written: pass copies of these")
         st = stream if stream is not None else torch.cuda.current_stream()
         weighted = self.post_weight is not None
         L.moe_combine_norm_backward(

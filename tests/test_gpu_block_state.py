@@ -206,3 +206,22 @@ def test_replay_with_a_balance_term(what):
     g.replay()
     same(results(), want)
     assert all((t == 7).all() for t in room)
+
+
+def test_gradient_in_the_layers_own_buffers():
+    """dy comes down the residual path too, after the layer's backward: it
+    cannot lie in what that writes.  It can be the block's own dx."""
+    layer = LAYERS["bf16"]()
+    block = M.MoEBlock(layer, weight(), EPS)
+    x, add, dy = batch(1, torch.bfloat16)
+    block.forward(x, add)
+    want = gradients(block, dy, x)
+    f, bb = block.buffers(CFG.T, x.dtype), layer.backward_buffers(CFG.T)
+    for t in (bb.dx_total, bb.dx, bb.dD[:CFG.T], bb.dxp[:CFG.T]):
+        t.copy_(dy)
+        with pytest.raises(ValueError, match="copies"):
+            block.backward(t, x)
+        with pytest.raises(ValueError, match="copies"):
+            block.backward(dy, t)
+    f.dx.copy_(dy)
+    same(gradients(block, f.dx, x), want)
